@@ -11,6 +11,7 @@ library's ``uint32`` words) and fp16 as ``torch.float16``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -20,13 +21,15 @@ __all__ = ["WQError", "lib", "quantize_group_int4", "quantize_int8_per_channel",
            "smooth", "smooth_workspace_bytes", "smooth_noalloc", "gemv_w4a16", "gemm_w4a16", "gemm_w8a8", "gemv_w8a16",
            "matmul_w4a16", "quantize_fp8_e4m3", "gemm_fp8", "outlier_columns", "gather_outliers",
            "gemm_w8a8_outliers", "llm_int8_matmul", "quantize_mxfp4", "quantize_nvfp4", "gemm_fp4",
-           "gemv_w4a16_bf16", "gemm_w4a16_bf16", "hessian", "gptq_prepare", "gptq_quantize", "awq", "device_status", "set_wait_limit",
+           "gemv_w4a16_bf16", "gemm_w4a16_bf16", "hessian", "gptq_prepare", "gptq_quantize", "awq",
+           "moe_route", "moe_route_workspace_bytes", "grouped_gemm_w4a16", "grouped_gemm_w8a8", "grouped_gemm_fp8",
+           "moe_combine", "moe_mlp_w4a16", "moe_mlp_w8a8", "device_status", "set_wait_limit",
            "selftest_wait_timeout", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libwq.so")
 
 WQ_OK, WQ_ERR_INVALID_ARG, WQ_ERR_ALIGNMENT, WQ_ERR_UNSUPPORTED, WQ_ERR_CUDA, WQ_ERR_TIMEOUT = range(6)
-WQ_F32, WQ_F16 = 0, 1
+WQ_F32, WQ_F16, WQ_BF16 = 0, 1, 2
 _STATUS = {0: "WQ_OK", 1: "WQ_ERR_INVALID_ARG", 2: "WQ_ERR_ALIGNMENT", 3: "WQ_ERR_UNSUPPORTED",
            4: "WQ_ERR_CUDA", 5: "WQ_ERR_TIMEOUT"}
 
@@ -67,6 +70,12 @@ _SIGS = {
     "wq_gptq_prepare": [_P, _I, _F, _P, _P, _P],
     "wq_gptq_quantize": [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P],
     "wq_awq": [_P, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P],
+    "wq_moe_route": [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P],
+    "wq_grouped_gemm_w4a16": [_P, _I, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P],
+    "wq_grouped_gemm_w4a16_bf16": [_P, _I, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P],
+    "wq_grouped_gemm_w8a8": [_P, _P, _I, _P, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P],
+    "wq_grouped_gemm_fp8": [_P, _P, _I, _I, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P],
+    "wq_moe_combine": [_P, _I, _I, _P, _P, _I, _I, _I, _P, _P],
     "wq_device_status": [_P],
     "wq_selftest_wait_timeout": [_P],
 }
@@ -84,6 +93,8 @@ lib.wq_fp4_scale_bytes.argtypes = [_I, _I, _I]
 lib.wq_fp4_scale_bytes.restype = ctypes.c_size_t
 lib.wq_awq_workspace_bytes.argtypes = [_I, _I]
 lib.wq_awq_workspace_bytes.restype = ctypes.c_size_t
+lib.wq_moe_route_workspace_bytes.argtypes = [_I, _I]
+lib.wq_moe_route_workspace_bytes.restype = ctypes.c_size_t
 lib.wq_set_wait_limit.argtypes = [ctypes.c_uint64]
 lib.wq_set_wait_limit.restype = None
 
@@ -504,6 +515,189 @@ def awq(w: torch.Tensor, x: torch.Tensor, grid=None, group_size: int = 128, stre
     _check(lib.wq_awq(_ptr(w), N, K, group_size, _ptr(x), T, garr, len(g), _ptr(qw), _ptr(sc), _ptr(qz), _ptr(s),
                       _ptr(err), _ptr(best), _ptr(ws), _P(_stream(stream))), "wq_awq")
     return qw, sc, qz, s, err, best
+
+
+# --------------------------------------------------------------------------
+# mixture-of-experts layers
+# --------------------------------------------------------------------------
+_HERE = contextlib.nullcontext()
+_DTYPE = {torch.float32: WQ_F32, torch.float16: WQ_F16, torch.bfloat16: WQ_BF16}
+
+
+def _on(t: torch.Tensor, stream):
+    """Context in which outputs and scratch of a call on `t` are allocated and its kernels launched: t's device,
+    and `stream` where one is given (so that scratch freed at the end of the call is not reused before it is done)."""
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+        return torch.cuda.stream(stream)
+    return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _with(first: torch.Tensor, t: torch.Tensor, name: str, dtypes, shape) -> torch.Tensor:
+    """`t` checked like `_cuda`, to have `shape` and to be on the device of `first`."""
+    _cuda(t, name, dtypes)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != first.device:
+        raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+    return t
+
+
+def moe_route_workspace_bytes(T: int, E: int) -> int:
+    return int(lib.wq_moe_route_workspace_bytes(int(T), int(E)))
+
+
+def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, workspace: torch.Tensor | None = None,
+              stream=None):
+    """Router: top-k experts per token, their softmax weights and the grouping of the (token, choice) pairs by expert.
+
+    logits [T, E] fp32, fp16 or bf16 -> (ids int32 [T, k], weights fp32 [T, k], offsets int32 [E + 1],
+    rows int32 [T * k], slots int32 [T, k]).  Equal logits go to the lowest expert; NaN and -inf are never chosen
+    (id -1, weight 0, slot -1 where nothing is left).  Expert e's sorted rows are offsets[e]:offsets[e + 1]."""
+    _cuda(logits, "logits", (torch.float32, torch.float16, torch.bfloat16), 2)
+    T, E = logits.shape
+    k = int(top_k)
+    with _on(logits, stream):
+        ids = _empty((T, max(k, 0)), torch.int32, logits)
+        weights = _empty((T, max(k, 0)), torch.float32, logits)
+        offsets = _empty((E + 1,), torch.int32, logits)
+        rows = _empty((T * max(k, 0),), torch.int32, logits)
+        slots = _empty((T, max(k, 0)), torch.int32, logits)
+        need = moe_route_workspace_bytes(T, E)
+        if workspace is None:
+            workspace = _empty((need,), torch.uint8, logits) if need else None
+        else:
+            _cuda(workspace, "workspace", (torch.uint8,), 1)
+            if workspace.numel() < need or workspace.device != logits.device:
+                raise ValueError(f"workspace must hold {need} bytes on {logits.device}")
+        _check(lib.wq_moe_route(_ptr(logits), _DTYPE[logits.dtype], T, E, k, int(bool(renormalize)), _ptr(ids),
+                                _ptr(weights), _ptr(offsets), _ptr(rows), _ptr(slots), _ptr(workspace),
+                                _P(_stream())), "wq_moe_route")
+    return ids, weights, offsets, rows, slots
+
+
+def _grouped_rows(x, offsets, rows, E):
+    """(T, R) of a grouped product: rows of x, sorted rows."""
+    _with(x, offsets, "offsets", (torch.int32,), (E + 1,))
+    if rows is None:
+        return x.shape[0], x.shape[0]
+    _with(x, rows, "rows", (torch.int32,), (rows.numel(),))
+    return x.shape[0], rows.numel()
+
+
+def _grouped_out(x, out, R, N, swiglu, dtype):
+    if swiglu and N % 2:
+        raise ValueError("the weights must have an even number of rows with swiglu")
+    shape = (R, N // 2 if swiglu else N)
+    return _empty(shape, dtype, x) if out is None else _with(x, out, "out", (dtype,), shape)
+
+
+def grouped_gemm_w4a16(x, qweight, scales, qzeros, offsets, rows=None, group_size: int = 128, swiglu: bool = False,
+                       out=None, stream=None):
+    """Expert products with packed INT4 weights: y[p] = dequant(W_e) x[rows[p]] for the sorted rows p of expert e.
+
+    x [T, K] fp16 or bf16; qweight int32 [E, N, K/8], scales fp16 [E, N, K/g], qzeros int32 [E, N, ceil(K/g/8)] (the
+    stacked outputs of quantize_group_int4); offsets int32 [E + 1] and rows int32 [R] as moe_route gives them (rows
+    None: the rows of x are sorted already).  swiglu: N = 2 I, y = silu(gate) * up of rows i and I + i.
+    -> [R, N or I] in x's dtype; rows outside the experts' ranges are not written."""
+    _cuda(x, "x", (torch.float16, torch.bfloat16), 2)
+    _cuda(qweight, "qweight", (torch.int32,), 3)
+    E, N, words = qweight.shape
+    K = x.shape[1]
+    if words * 8 != K or group_size <= 0 or K % group_size:
+        raise ValueError("qweight must be [E, N, K/8] and K a multiple of group_size")
+    _with(x, qweight, "qweight", (torch.int32,), (E, N, K // 8))
+    _with(x, scales, "scales", (torch.float16,), (E, N, K // group_size))
+    _with(x, qzeros, "qzeros", (torch.int32,), (E, N, (K // group_size + 7) // 8))
+    T, R = _grouped_rows(x, offsets, rows, E)
+    bf16 = x.dtype == torch.bfloat16
+    fn = lib.wq_grouped_gemm_w4a16_bf16 if bf16 else lib.wq_grouped_gemm_w4a16
+    with _on(x, stream):
+        y = _grouped_out(x, out, R, N, swiglu, x.dtype)
+        _check(fn(_ptr(x), T, _ptr(rows), _ptr(offsets), R, _ptr(qweight), _ptr(scales), _ptr(qzeros), E, N, K,
+                  group_size, int(bool(swiglu)), _ptr(y), _P(_stream())),
+               "wq_grouped_gemm_w4a16_bf16" if bf16 else "wq_grouped_gemm_w4a16")
+    return y
+
+
+def grouped_gemm_w8a8(xq, sx, wq, sw, offsets, rows=None, swiglu: bool = False, out=None, stream=None):
+    """Expert products in INT8: y[p] = fp16((xq[t] @ wq[e]^T) * sx[t] * sw[e]), t = rows[p], for expert e's rows p.
+
+    xq int8 [T, K], sx fp32 [T] (quantize_int8_per_token); wq int8 [E, N, K], sw fp32 [E, N] (stacked
+    quantize_int8_per_channel); offsets, rows, swiglu and the result as for grouped_gemm_w4a16 (fp16)."""
+    _cuda(xq, "xq", (torch.int8,), 2)
+    _cuda(wq, "wq", (torch.int8,), 3)
+    E, N, K = wq.shape
+    T, R = _grouped_rows(xq, offsets, rows, E)
+    _with(xq, wq, "wq", (torch.int8,), (E, N, xq.shape[1]))
+    _with(xq, sx, "sx", (torch.float32,), (T,))
+    _with(xq, sw, "sw", (torch.float32,), (E, N))
+    with _on(xq, stream):
+        y = _grouped_out(xq, out, R, N, swiglu, torch.float16)
+        _check(lib.wq_grouped_gemm_w8a8(_ptr(xq), _ptr(sx), T, _ptr(rows), _ptr(offsets), R, _ptr(wq), _ptr(sw), E, N,
+                                        K, int(bool(swiglu)), _ptr(y), _P(_stream())), "wq_grouped_gemm_w8a8")
+    return y
+
+
+def grouped_gemm_fp8(xq, sx, wq, sw, offsets, rows=None, swiglu: bool = False, out=None, stream=None):
+    """Expert products in FP8 E4M3 (codes as uint8): as grouped_gemm_w8a8, with sx fp32 [T] or [1] and sw fp32
+    [E, N] or [E] (per token or per tensor; per channel or per expert)."""
+    _cuda(xq, "xq", (torch.uint8,), 2)
+    _cuda(wq, "wq", (torch.uint8,), 3)
+    E, N, K = wq.shape
+    T, R = _grouped_rows(xq, offsets, rows, E)
+    _with(xq, wq, "wq", (torch.uint8,), (E, N, xq.shape[1]))
+    if tuple(sx.shape) not in ((T,), (1,)) or tuple(sw.shape) not in ((E, N), (E,)):
+        raise ValueError("shape mismatch: sx must be [T] or [1], sw [E, N] or [E]")
+    _with(xq, sx, "sx", (torch.float32,), sx.shape)
+    _with(xq, sw, "sw", (torch.float32,), sw.shape)
+    with _on(xq, stream):
+        y = _grouped_out(xq, out, R, N, swiglu, torch.float16)
+        _check(lib.wq_grouped_gemm_fp8(_ptr(xq), _ptr(sx), int(sx.numel() == T), T, _ptr(rows), _ptr(offsets), R,
+                                       _ptr(wq), _ptr(sw), int(sw.dim() == 2), E, N, K, int(bool(swiglu)), _ptr(y),
+                                       _P(_stream())), "wq_grouped_gemm_fp8")
+    return y
+
+
+def moe_combine(y, weights, slots, out=None, stream=None):
+    """out [T, N] = sum_j weights[t, j] * y[slots[t, j]] (fp32 sums, one rounding); slots outside y add nothing.
+
+    y [R, N] fp16 or bf16; weights fp32 [T, k] and slots int32 [T, k] as moe_route gives them."""
+    _cuda(y, "y", (torch.float16, torch.bfloat16), 2)
+    _cuda(slots, "slots", (torch.int32,), 2)
+    T, k = slots.shape
+    R, N = y.shape
+    _with(y, slots, "slots", (torch.int32,), (T, k))
+    _with(y, weights, "weights", (torch.float32,), (T, k))
+    with _on(y, stream):
+        o = _empty((T, N), y.dtype, y) if out is None else _with(y, out, "out", (y.dtype,), (T, N))
+        _check(lib.wq_moe_combine(_ptr(y), _DTYPE[y.dtype], R, _ptr(weights), _ptr(slots), T, k, N, _ptr(o),
+                                  _P(_stream())), "wq_moe_combine")
+    return o
+
+
+def moe_mlp_w4a16(x, logits, gate_up, down, top_k: int, group_size: int = 128, renormalize: bool = True, stream=None):
+    """A mixture-of-experts feed-forward layer with INT4 experts: router, gate and up projection with SwiGLU, down
+    projection, combine.  x [T, K] fp16 or bf16, logits [T, E]; gate_up and down are (qweight, scales, qzeros) stacked
+    over the experts, [E, 2 I, ...] over K and [E, N, ...] over I.  -> [T, N] in x's dtype."""
+    with _on(x, stream):
+        _, weights, offsets, rows, slots = moe_route(logits, top_k, renormalize)
+        h = grouped_gemm_w4a16(x, *gate_up, offsets, rows, group_size, swiglu=True)
+        y = grouped_gemm_w4a16(h, *down, offsets, None, group_size)
+        return moe_combine(y, weights, slots)
+
+
+def moe_mlp_w8a8(x, logits, gate_up, down, top_k: int, renormalize: bool = True, stream=None):
+    """The same layer with INT8 experts: x fp16 [T, K] and the SwiGLU outputs are quantized per token; gate_up and
+    down are (wq, sw) stacked over the experts.  -> fp16 [T, N]."""
+    with _on(x, stream):
+        _, weights, offsets, rows, slots = moe_route(logits, top_k, renormalize)
+        xq, sx = quantize_int8_per_token(x)
+        h = grouped_gemm_w8a8(xq, sx, *gate_up, offsets, rows, swiglu=True)
+        hq, sh = quantize_int8_per_token(h)
+        y = grouped_gemm_w8a8(hq, sh, *down, offsets)
+        return moe_combine(y, weights, slots)
 
 
 def device_status(stream=None) -> int:

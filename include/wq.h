@@ -60,7 +60,7 @@ typedef enum {
     WQ_ERR_TIMEOUT = 5      /* a bounded wait inside a kernel ran out */
 } wq_status;
 
-typedef enum { WQ_F32 = 0, WQ_F16 = 1 } wq_dtype;
+typedef enum { WQ_F32 = 0, WQ_F16 = 1, WQ_BF16 = 2 } wq_dtype;
 
 /*
  * Asymmetric INT4 per-group quantization.
@@ -417,6 +417,87 @@ size_t wq_awq_workspace_bytes(int N, int K);
 wq_status wq_awq(const uint16_t *w, int N, int K, int group_size, const uint16_t *x, int T, const double *grid,
                  int ngrid, uint32_t *qweight, uint16_t *scales, uint32_t *qzeros, float *s, double *err, int *best,
                  void *workspace, void *stream);
+
+/*
+ * Mixture-of-experts layers with quantized experts.  A layer has E experts,
+ * each an nn.Linear weight [N][K] of one of the formats above, stacked to
+ * [E][N][K]; each of T tokens goes to top_k of them.  The sequence is:
+ *   wq_moe_route        logits -> ids, weights, offsets, rows, slots
+ *   wq_grouped_gemm_*   gate and up projection of the sorted rows (rows given,
+ *                       swiglu = 1), then the down projection (rows NULL)
+ *   wq_moe_combine      weighted sum of each token's rows
+ * The T * top_k (token, choice) pairs are sorted by expert: the sorted rows of
+ * expert e are offsets[e] .. offsets[e + 1] - 1, rows[p] is the token of sorted
+ * row p and slots[t][j] the sorted row of token t's j-th choice.  All of it
+ * stays on the device: no call reads offsets on the host.  The pages stop at
+ * dense layers; the formats, scales and rounding are theirs.
+ *
+ * wq_moe_route: the router.  A logit is selectable when it is neither NaN nor
+ * -inf.  ids[t] are the top_k selectable experts with the largest logits,
+ * largest first and the lowest expert first among equal ones; where fewer are
+ * selectable, the rest are -1.  weights[t][j] = exp(l_j) / sum exp(l), the sum
+ * over the chosen experts (renormalize != 0) or over all selectable ones
+ * (0), computed in fp32 relative to the largest logit (experts at +inf share
+ * the weight among themselves); 0 where the id is -1.  Within an expert the
+ * rows are in token order.  Pairs without an expert come after the last one:
+ * rows is -1 there and their slots are -1.  The result does not depend on
+ * scheduling.
+ * logits: [T][E] of dtype WQ_F32, WQ_F16 or WQ_BF16;  ids: out int32
+ * [T][top_k];  weights: out fp32 [T][top_k];  offsets: out int32 [E + 1];
+ * rows: out int32 [T * top_k];  slots: out int32 [T][top_k].  workspace:
+ * wq_moe_route_workspace_bytes(T, E) bytes (0, and NULL is taken, for T <= 128),
+ * 16-byte aligned, contents on entry do not matter; calls that share one must not overlap on the GPU.
+ * 1 <= top_k <= min(E, 32), E <= 512, T * top_k < 2^31.
+ */
+size_t wq_moe_route_workspace_bytes(int T, int E);
+wq_status wq_moe_route(const void *logits, wq_dtype dtype, int T, int E, int top_k, int renormalize, int32_t *ids,
+                       float *weights, int32_t *offsets, int32_t *rows, int32_t *slots, void *workspace,
+                       void *stream);
+
+/*
+ * Expert products.  For every expert e and sorted row p of its range,
+ *   d[n] = sum_k W_e[n][k] * x[rows ? rows[p] : p][k]
+ *   y[p][n] = round(d[n])                             (swiglu == 0, y [R][N])
+ *   y[p][i] = round(silu(d[i]) * d[N/2 + i])          (swiglu != 0, y [R][N/2])
+ * with silu(g) = g / (1 + exp(-g)) in fp32 and one rounding.  d per format:
+ *   w4a16, w4a16_bf16:  W_e[n][k] = s (q - z), each rounded to the type of x
+ *       (fp16, bf16) before the product, fp32 accumulation (order unspecified)
+ *   w8a8:  (float)(int32 sum of codes) * sx[token] * sw[e][n]
+ *   fp8:   the same with E4M3 codes and an fp32 sum; sx is [T] or [1]
+ *       (sx_per_row), sw [E][N] or [E], one per expert (sw_per_row)
+ * x (xq): [T] rows;  rows: int32 [R] or NULL for the rows of x in order (then
+ * R == T);  offsets: int32 [E + 1], non-decreasing within [0, R];  weights
+ * stacked over e in the layouts above.  Rows of y before offsets[0] and from
+ * offsets[E] on are not written.  An entry of rows outside [0, T) gives a row
+ * of zeros; offsets outside their range are clamped to it and made
+ * non-decreasing, so that no value of either reads or writes out of bounds.
+ * A NaN or infinity in a row of x stays in that row of y.
+ * E <= 512, E * N < 2^31.  w4a16: group_size in {32, 64, 128, 256}, K a
+ * multiple of it.  w8a8 and fp8: K % 16 == 0 (w8a8: K <= 131056).  swiglu:
+ * N even.
+ */
+wq_status wq_grouped_gemm_w4a16(const uint16_t *x, int T, const int32_t *rows, const int32_t *offsets, int R,
+                                const uint32_t *qweight, const uint16_t *scales, const uint32_t *qzeros, int E, int N,
+                                int K, int group_size, int swiglu, uint16_t *y, void *stream);
+wq_status wq_grouped_gemm_w4a16_bf16(const uint16_t *x, int T, const int32_t *rows, const int32_t *offsets, int R,
+                                     const uint32_t *qweight, const uint16_t *scales, const uint32_t *qzeros, int E,
+                                     int N, int K, int group_size, int swiglu, uint16_t *y, void *stream);
+wq_status wq_grouped_gemm_w8a8(const int8_t *xq, const float *sx, int T, const int32_t *rows, const int32_t *offsets,
+                               int R, const int8_t *wq, const float *sw, int E, int N, int K, int swiglu, uint16_t *y,
+                               void *stream);
+wq_status wq_grouped_gemm_fp8(const uint8_t *xq, const float *sx, int sx_per_row, int T, const int32_t *rows,
+                              const int32_t *offsets, int R, const uint8_t *wq, const float *sw, int sw_per_row, int E,
+                              int N, int K, int swiglu, uint16_t *y, void *stream);
+
+/*
+ * Combine: out[t][n] = round( sum_j weights[t][j] * y[slots[t][j]][n] ), summed
+ * in fp32 in the order of j; a slot outside [0, R) (a choice without an
+ * expert) adds nothing, so a token without any gives zeros.
+ * y: [R][N] and out: [T][N] of dtype WQ_F16 or WQ_BF16;  weights: fp32
+ * [T][top_k];  slots: int32 [T][top_k].  out must not overlap y.
+ */
+wq_status wq_moe_combine(const uint16_t *y, wq_dtype dtype, int R, const float *weights, const int32_t *slots, int T,
+                         int top_k, int N, uint16_t *out, void *stream);
 
 /* Message describing the last error status returned on this host thread. */
 const char *wq_last_error(void);
