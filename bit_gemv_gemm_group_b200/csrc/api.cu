@@ -74,9 +74,8 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 }  // namespace
 
-bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, int elem_bytes, const void *base, uint64_t inner,
-                    uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
-                    CUtensorMapSwizzle swizzle) {
+bool encode_tmap(CUtensorMap *map, CUtensorMapDataType dtype, int rank, const void *base, const uint64_t *dims,
+                 const uint64_t *strides, const uint32_t *box, CUtensorMapSwizzle swizzle) {
     std::call_once(g_encode_once, [] {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
@@ -88,19 +87,30 @@ bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, int elem_bytes,
         fail(WQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
         return false;
     }
-    const cuuint64_t dims[2] = {inner, outer};
-    const cuuint64_t strides[1] = {row_bytes};
-    const cuuint32_t box[2] = {box_inner, box_outer};
-    const cuuint32_t estr[2] = {1, 1};
-    (void)elem_bytes;
-    CUresult r = g_encode(map, dtype, 2, const_cast<void *>(base), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    cuuint64_t d[5], st[4];
+    cuuint32_t bx[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        bx[i] = box[i];
+        if (i) st[i - 1] = strides[i - 1];
+    }
+    CUresult r = g_encode(map, dtype, rank, const_cast<void *>(base), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         fail(WQ_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
         return false;
     }
     return true;
+}
+
+bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, int elem_bytes, const void *base, uint64_t inner,
+                    uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+                    CUtensorMapSwizzle swizzle) {
+    (void)elem_bytes;
+    const uint64_t dims[2] = {inner, outer}, strides[1] = {row_bytes};
+    const uint32_t box[2] = {box_inner, box_outer};
+    return encode_tmap(map, dtype, 2, base, dims, strides, box, swizzle);
 }
 
 }  // namespace wq

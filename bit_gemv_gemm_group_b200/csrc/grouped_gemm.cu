@@ -6,21 +6,30 @@
 // with W and x in INT8 (per-token x per-channel scales), FP8 E4M3 (the same) or W packed INT4 with x in
 // fp16 / bf16; optionally N = 2 I and y[p][i] = silu(gate) up of rows i and I + i of W.
 //
-// Swap-AB: the MMA's M dimension is 128 weight rows (TMEM lanes), its N dimension the activation rows of
-// one expert, so that a ragged group costs its own length rounded up to 16 and not to a 128-row tile.  An
-// expert's rows are cut into blocks of at most 256 of nearly equal length; a tile is (expert, row block,
-// 128 weight rows), row blocks innermost so that the CTAs that run together share weight tiles in L2.
-// Every CTA derives the tile list from the offsets in device memory, so the host never waits for them.
+// Swap-AB: the MMA's M dimension is weight rows (TMEM lanes), its N dimension the activation rows of one
+// expert, so that a ragged group costs its own length rounded up to 16 or 32 and not to a 128-row tile.  An
+// expert's rows are cut into blocks of nearly equal length; a tile is (expert, row block, weight rows), row
+// blocks innermost so that the CTAs that run together share weight tiles in L2.  Every CTA derives the tile
+// list from the offsets in device memory, so the host never waits for them.
+//
+// Two shapes (see choose_pair):
+//   pair    two CTAs per tile of 256 weight rows and up to 256 activation rows (cta_group::2): each CTA
+//           brings 128 weight rows and half of the activation rows, so a stage moves two thirds of the
+//           bytes that a CTA of its own would move for the same MMA
+//   single  one CTA per tile of 128 weight rows and up to 64 activation rows with a deeper ring: few rows
+//           per expert, where the weights' bytes are all that counts
 //
 // Persistent warp-specialized CTA, one per SM:
-//   warp 0      activations into a shared-memory ring (128-byte swizzle): TMA gather of four indexed rows
-//               per request (tile::gather4), the 32 lanes each issuing their share, or 32-row boxes when
-//               the rows already lie in order; for 8-bit weights also the weight tile
-//   warp 1      one thread issues tcgen05.mma into one of two 256-column fp32/int32 accumulators
+//   warp 0      TMA: weight tiles (8-bit kinds) and, when the rows lie in order, activations
+//   warp 1      an elected thread issues tcgen05.mma into one of two accumulators; in the pair's second CTA it
+//               passes on to the first that a stage is filled
 //   warp 2      allocates tensor memory
-//   warp 3      (INT4) packed weight tiles, 128 rows x 32 bytes, into a ring of their own
+//   warp 3      (INT4) packed weight tiles, 128 rows x 128 bytes (four stages), into a ring of their own:
+//               with 32-byte rows a TMA request took about 1000 cycles for its 4 KB
 //   warps 4-7   epilogue of the previous tile: scales, SwiGLU, conversion, stores
-//   warps 8-15  (INT4) dequantize packed tiles into the weight operand's shared-memory stage
+//   then        four warps that gather indexed activation rows by cp.async (TMA's gather of four rows a
+//               request took 32 cycles for its 512 bytes, four times what the MMAs leave), and for INT4
+//               four groups of four warps that dequantize every fourth stage each
 #include "sm100.cuh"
 #include "wq_device.cuh"
 #include "wq_host.h"
@@ -35,23 +44,24 @@ using namespace sm100;
 
 enum Kind { K_I8, K_FP8, K_W4H, K_W4B };  // INT8, E4M3, INT4 weights with fp16 / bf16 activations
 
-constexpr int BM = 128;                // weight rows of a tile
-constexpr int BR = 256;                // activation rows of a tile, at most
+constexpr int BM = 128;                // weight rows of a CTA's share of a tile
 constexpr int STAGE_K = 128;           // bytes of k per stage and row (128 INT8/FP8 or 64 16-bit values)
-constexpr int STAGES = 4;
-constexpr int PSTAGES = 6;             // packed INT4 tiles
-constexpr uint32_t A_BYTES = BM * STAGE_K, B_BYTES = BR * STAGE_K, P_BYTES = BM * 32;
-constexpr int BOX_ROWS = 32;           // rows per box when the activations lie in order
+constexpr uint32_t A_BYTES = BM * STAGE_K;
+constexpr int PK = 4;                  // stages per packed INT4 tile (128 bytes of a weight row)
+constexpr uint32_t P_BYTES = BM * PK * 32;
 constexpr int MAX_E = 512;
-constexpr int EPI_WARP0 = 4, DQ_WARP0 = 8, DQ_WARPS = 8;
+constexpr int EPI_WARP0 = 4, GATHER_WARPS = 4, DQ_GROUPS = 4;
+constexpr int LAG = 2;                 // stages of gathered rows in flight per thread
+constexpr int MAX_STAGES = 8, MAX_PSTAGES = 4;
 constexpr uint64_t DRAIN_NS = 2000000000ull;
 constexpr unsigned SITE_PRODUCER = 0x1001, SITE_MMA = 0x1002, SITE_EPILOGUE = 0x1004, SITE_DRAIN = 0x1008,
-                   SITE_DEQUANT = 0x1010, SITE_PACKED = 0x1020;
+                   SITE_DEQUANT = 0x1010, SITE_PACKED = 0x1020, SITE_GATHER = 0x1040;
 
 struct Bars {
-    uint64_t full[STAGES], empty[STAGES];   // copies of a stage landed / its MMAs done
-    uint64_t dq_full[STAGES];               // INT4: dequantized weight tile of the stage written
-    uint64_t pk_full[PSTAGES], pk_empty[PSTAGES];
+    uint64_t full[MAX_STAGES], empty[MAX_STAGES];  // TMA copies of a stage landed / its MMAs done
+    uint64_t put[MAX_STAGES];  // what warps write of a stage: gathered rows and dequantized weights (an arrival
+                               // per warp) and, in a pair's first CTA, word that the second's share is there
+    uint64_t pk_full[MAX_PSTAGES], pk_empty[MAX_PSTAGES];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
     uint32_t tmem_base;
@@ -60,21 +70,32 @@ struct Bars {
 
 __host__ __device__ constexpr bool is_w4(Kind k) { return k == K_W4H || k == K_W4B; }
 
-template <Kind KIND>
+template <Kind KIND, bool GATHER, bool PAIR>
 struct Layout {
     static constexpr bool W4 = is_w4(KIND);
-    static constexpr int THREADS = W4 ? 512 : 256;
+    static constexpr int BR = PAIR ? 256 : 64;               // activation rows of a tile, at most
+    static constexpr int SR = PAIR ? BR / 2 : BR;            // of them in this CTA's shared memory
+    static constexpr uint32_t B_BYTES = SR * STAGE_K;
+    static constexpr int STAGES = PAIR ? (W4 ? 5 : 6) : (W4 ? 6 : 8);
+    static constexpr int PSTAGES = PAIR ? 3 : 4;             // packed INT4 tiles
+    static constexpr int BOX = PAIR ? 64 : 16;               // rows per box when the activations lie in order
+    static constexpr int GA_WARP0 = 8;
+    static constexpr int DQ_WARP0 = GA_WARP0 + (GATHER ? GATHER_WARPS : 0);
+    static constexpr int THREADS = 32 * (DQ_WARP0 + (W4 ? 4 * DQ_GROUPS : 0));
     static constexpr uint32_t OFF_B = STAGES * A_BYTES;
     static constexpr uint32_t OFF_P = OFF_B + STAGES * B_BYTES;
     static constexpr uint32_t OFF_BAR = OFF_P + (W4 ? PSTAGES * P_BYTES : 0);
-    static constexpr uint32_t OFF_SRC = OFF_BAR + 512;                    // int [2][BR]: token of each row
+    static constexpr uint32_t OFF_SRC = OFF_BAR + 1024;                   // int [2][BR]: token of each row
     static constexpr uint32_t OFF_SX = OFF_SRC + 2 * BR * 4;              // float [2][BR] (8-bit kinds)
     static constexpr uint32_t OFF_TAB = OFF_SX + (W4 ? 0 : 2 * BR * 4);   // int offsets[E + 1], tiles[E + 1]
-    static size_t smem(int E) { return 1024 + OFF_TAB + 2 * (size_t)(E + 1) * 4; }
+    static constexpr size_t smem(int E) { return 1024 + OFF_TAB + 2 * (size_t)(E + 1) * 4; }
+    static_assert(smem(MAX_E) <= 232448, "fits the shared memory of a CTA");
+    static_assert(STAGES <= MAX_STAGES && PSTAGES <= MAX_PSTAGES && STAGES > LAG, "barrier arrays, gather lag");
 };
-static_assert(sizeof(Bars) <= 512, "barriers fit their space");
+static_assert(sizeof(Bars) <= 1024, "barriers fit their space");
 
 struct Args {
+    const uint8_t *x;                // [T] rows
     const int32_t *offsets, *rows;   // rows null: row p of x itself
     const float *sx, *sw;
     int sx_stride, sw_per_row;
@@ -83,6 +104,7 @@ struct Args {
     uint16_t *y;
     int T, R, E, N, K, gs;           // T: rows of x, R: grouped rows
     int nb;                          // weight-row blocks per expert
+    int box;                         // SwiGLU: the weight map is the 5-D one (see load_weights)
     int ldy;                         // columns of y (N, or N / 2 with SwiGLU)
     unsigned int *status;
     uint64_t limit_ns;
@@ -93,10 +115,9 @@ struct Tile {
     int r0, rows;     // first grouped row, number of rows
 };
 
-__device__ __forceinline__ int row_blocks(int n) { return (n + BR - 1) / BR; }
-
 // Offsets clamped to [0, R] and made non-decreasing (a valid array is unchanged), and the exclusive
 // prefix of the experts' tile counts; by one warp.
+template <int BR>
 __device__ __forceinline__ void build_table(const Args &a, int *off, int *tiles, int lane) {
     int high = 0;
     for (int i0 = 0; i0 <= a.E; i0 += 32) {
@@ -110,7 +131,7 @@ __device__ __forceinline__ void build_table(const Args &a, int *off, int *tiles,
     __syncwarp();
     int run = 0;
     for (int i0 = 0; i0 < a.E; i0 += 32) {
-        const int v = i0 + lane < a.E ? row_blocks(off[i0 + lane + 1] - off[i0 + lane]) * a.nb : 0;
+        const int v = i0 + lane < a.E ? (off[i0 + lane + 1] - off[i0 + lane] + BR - 1) / BR * a.nb : 0;
         int s = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -123,8 +144,9 @@ __device__ __forceinline__ void build_table(const Args &a, int *off, int *tiles,
     if (lane == 0) tiles[a.E] = run;
 }
 
-// Tile t of the list; false past its end.  BN: output columns per tile.
-template <int BN>
+// Tile t of the list; false past its end.  BN: output columns per tile, BR and STEP: most rows of a block
+// and what its length is rounded up to.
+template <int BN, int BR, int STEP>
 __device__ __forceinline__ bool get_tile(const Args &a, const int *off, const int *tiles, int t, Tile &w) {
     if (t >= tiles[a.E]) return false;
     int lo = 0, hi = a.E;  // the expert e with tiles[e] <= t < tiles[e + 1]
@@ -133,8 +155,8 @@ __device__ __forceinline__ bool get_tile(const Args &a, const int *off, const in
         if (tiles[mid] <= t) lo = mid;
         else hi = mid;
     }
-    const int first = off[lo], n = off[lo + 1] - first, rb = row_blocks(n);
-    const int per = ((n + rb - 1) / rb + 15) & ~15;
+    const int first = off[lo], n = off[lo + 1] - first, rb = (n + BR - 1) / BR;
+    const int per = ((n + rb - 1) / rb + STEP - 1) / STEP * STEP;
     const int local = t - tiles[lo], b = local % rb;
     w.e = lo;
     w.n0 = (local / rb) * BN;
@@ -143,27 +165,23 @@ __device__ __forceinline__ bool get_tile(const Args &a, const int *off, const in
     return true;
 }
 
-// Four rows of a 2-D tensor (row indices r0..r3, elements from c0) into 4 consecutive 128-byte lines.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int r0, int r1,
-                                            int r2, int r3) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
-        : "memory");
-}
-
-template <Kind KIND>
+template <Kind KIND, bool PAIR>
 __device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    if (KIND == K_I8) mma_i8(d, a, b, idesc, acc);
-    else if (KIND == K_FP8) mma_f8f6f4(d, a, b, idesc, acc);
-    else mma_f16(d, a, b, idesc, acc);
+    if (PAIR) {
+        if (KIND == K_I8) mma_i8_pair(d, a, b, idesc, acc);
+        else if (KIND == K_FP8) mma_f8f6f4_pair(d, a, b, idesc, acc);
+        else mma_f16_pair(d, a, b, idesc, acc);
+    } else {
+        if (KIND == K_I8) mma_i8(d, a, b, idesc, acc);
+        else if (KIND == K_FP8) mma_f8f6f4(d, a, b, idesc, acc);
+        else mma_f16(d, a, b, idesc, acc);
+    }
 }
 
 template <Kind KIND>
-__host__ __device__ constexpr uint32_t idesc_rows(int rows) {
-    return KIND == K_I8 ? make_idesc(2, 1, 1, BM, rows)
-                        : make_idesc(1, KIND == K_W4B ? 1 : 0, KIND == K_W4B ? 1 : 0, BM, rows);
+__host__ __device__ constexpr uint32_t idesc_rows(int m, int rows) {
+    return KIND == K_I8 ? make_idesc(2, 1, 1, m, rows)
+                        : make_idesc(1, KIND == K_W4B ? 1 : 0, KIND == K_W4B ? 1 : 0, m, rows);
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -184,21 +202,53 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     return d;
 }
 
-// One word of 8 codes -> 8 weights s (q - z) in k order, each rounded once to the activations' type (the
-// tensor cores take both operands in one type).  A byte's two nibbles become 1024 + q and 1024 + 16 q in
-// one PRMT and one LOP3; an exact fma by (1, 1/16) with -(1024 + z), -(64 + z) leaves q - z.
+__device__ __forceinline__ uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// What a thread needs of a group's scale s and zero point z to dequantize its codes.
 template <bool BF>
-__device__ __forceinline__ uint4 dequant_word(uint32_t w, uint32_t zc, uint32_t s2, float s) {
+struct GroupConst {
+    uint32_t zc, hi, lo;
+    // fp16: -(1024 + z), -(64 + z) and s.  bf16: -(128 + z) twice, and s = hi + lo, two bf16 values that
+    // hold the 11 bits of s.
+    __device__ __forceinline__ void set(uint32_t s16, uint32_t z) {
+        if (BF) {
+            const float s = half_bits_to_float((uint16_t)s16);
+            const uint32_t h = float_to_bf16_bits_rn(s);
+            const uint32_t l = float_to_bf16_bits_rn(s - __uint_as_float(h << 16));
+            zc = 0xC300C300u + z * 0x00010001u;
+            hi = h * 0x00010001u;
+            lo = l * 0x00010001u;
+        } else {
+            zc = 0xD400E400u + z * 0x00100001u;
+            hi = s16 * 0x00010001u;
+            lo = 0;
+        }
+    }
+};
+
+// One word of 8 codes -> 8 weights s (q - z) in k order, each rounded once to the activations' type (the
+// tensor cores take both operands in one type).
+// fp16: a byte's two nibbles become 1024 + q and 1024 + 16 q by one PRMT and one LOP3, an exact fma by
+// (1, 1/16) with -(1024 + z), -(64 + z) leaves q - z, and one product rounds.
+// bf16: 128 + q has 8 bits, so a nibble can only sit in the lowest bits: the odd codes come from the word
+// shifted by 4.  (q - z) hi + (q - z) lo in one fma after a product whose own rounding is 2^-16 of the result.
+template <bool BF>
+__device__ __forceinline__ uint4 dequant_word(uint32_t w, const GroupConst<BF> &g) {
     uint32_t o[4];
+    const uint32_t w4 = w >> 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t h = (prmt(w, 0u, 0x4040u + 0x0101u * i) & 0x00F0000Fu) | 0x64006400u;
-        const uint32_t d = hfma2(h, 0x2C003C00u, zc);
         if (BF) {
-            const float2 f = half2_bits_to_float2(d);
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(__fmul_rn(f.y, s)), "f"(__fmul_rn(f.x, s)));
+            const uint32_t h = (prmt(w, w4, 0x4400u + 0x1111u * i) & 0x000F000Fu) | 0x43004300u;
+            const uint32_t d = bfma2(h, 0x3F803F80u, g.zc);
+            o[i] = bfma2(d, g.hi, bfma2(d, g.lo, 0x80008000u));
         } else {
-            o[i] = hmul2(d, s2);
+            const uint32_t h = (prmt(w, 0u, 0x4040u + 0x0101u * i) & 0x00F0000Fu) | 0x64006400u;
+            o[i] = hmul2(hfma2(h, 0x2C003C00u, g.zc), g.hi);
         }
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
@@ -223,16 +273,19 @@ __device__ __forceinline__ uint16_t out_bits(float v) {
     return KIND == K_W4B ? float_to_bf16_bits_rn(v) : float_to_half_bits_rn(v);
 }
 
-// SWIGLU: a tile's 128 weight rows are, per 32 TMEM lanes, 16 gate rows and the 16 up rows that belong to
+// SWIGLU: a CTA's 128 weight rows are, per 32 TMEM lanes, 16 gate rows and the 16 up rows that belong to
 // them, so gate and up of one output meet by a shuffle inside a warp.
-template <Kind KIND, bool GATHER, bool SWIGLU>
-__global__ void __launch_bounds__(Layout<KIND>::THREADS, 1)
+template <Kind KIND, bool GATHER, bool SWIGLU, bool PAIR>
+__global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                         const Args a) {
-    using L = Layout<KIND>;
-    constexpr bool W4 = L::W4;
-    constexpr int BN = SWIGLU ? BM / 2 : BM;           // output columns per tile
+    using L = Layout<KIND, GATHER, PAIR>;
+    constexpr bool W4 = L::W4, TMA_STAGE = !W4 || !GATHER;  // the stage's barrier `full` is used
+    constexpr int BR = L::BR, STEP = PAIR ? 32 : 16, STAGES = L::STAGES, PSTAGES = L::PSTAGES;
+    constexpr int BNC = SWIGLU ? BM / 2 : BM;          // output columns of this CTA's share of a tile
+    constexpr int BN = PAIR ? 2 * BNC : BNC;
     constexpr int KE = W4 ? STAGE_K / 2 : STAGE_K;     // k values per stage
+    constexpr uint32_t TMEM_COLS = 2 * BR;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Bars *bar = reinterpret_cast<Bars *>(base + L::OFF_BAR);
@@ -241,21 +294,23 @@ __global__ void __launch_bounds__(Layout<KIND>::THREADS, 1)
     int *off = reinterpret_cast<int *>(base + L::OFF_TAB), *tiles = off + a.E + 1;
     const uint32_t sA = smem_u32(base), sB = smem_u32(base + L::OFF_B), sP = smem_u32(base + L::OFF_P);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kst = (a.K + KE - 1) / KE;
+    const int rank = PAIR ? (int)cluster_ctarank() : 0;
+    const int first = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x, stride = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
+    const int kst = (a.K + KE - 1) / KE, packs = (kst + PK - 1) / PK;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&bar->full[s]), 1);
-            mbar_init(smem_u32(&bar->dq_full[s]), DQ_WARPS);
             mbar_init(smem_u32(&bar->empty[s]), 1);
+            mbar_init(smem_u32(&bar->put[s]), max(1, (GATHER ? GATHER_WARPS : 0) + (W4 ? 4 : 0) + (PAIR && rank == 0)));
         }
         for (int p = 0; p < PSTAGES; ++p) {
             mbar_init(smem_u32(&bar->pk_full[p]), 1);
-            mbar_init(smem_u32(&bar->pk_empty[p]), DQ_WARPS);
+            mbar_init(smem_u32(&bar->pk_empty[p]), 4 * DQ_GROUPS);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bar->acc_full[i]), 1);
-            mbar_init(smem_u32(&bar->acc_empty[i]), 4);
+            mbar_init(smem_u32(&bar->acc_empty[i]), PAIR ? 8 : 4);
         }
         mbar_init(smem_u32(&bar->drain), 1);
         bar->abort = 0;
@@ -265,141 +320,144 @@ __global__ void __launch_bounds__(Layout<KIND>::THREADS, 1)
         prefetch_tmap(&tmap_x);
         prefetch_tmap(&tmap_w);
     }
-    if (warp == 1) build_table(a, off, tiles, lane);
+    if (warp == 1) build_table<BR>(a, off, tiles, lane);
     if (warp == 2) {
-        tmem_alloc(smem_u32(&bar->tmem_base), 512);
-        tmem_relinquish();
+        if (PAIR) {
+            tmem_alloc_pair(smem_u32(&bar->tmem_base), TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(&bar->tmem_base), TMEM_COLS);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // the other CTA's barriers are set up before anything arrives on them
     tc_fence_after();
     const uint32_t tmem_base = bar->tmem_base;
     const WaitCtl ctl{&bar->abort, a.status, a.limit_ns};
     Tile w;
 
-    // First weight row (of the stacked [E N] rows) of lane group i (16 lanes) of tile w.
+    // First weight row (of the stacked [E N] rows) of lane group i (16 lanes) of this CTA's share of tile t.
     auto weight_row = [&](const Tile &t, int i) {
-        return t.e * a.N + t.n0 + (SWIGLU ? (i & 1) * (a.N / 2) + (i >> 1) * 16 : i * 16);
+        return t.e * a.N + t.n0 + rank * BNC + (SWIGLU ? (i & 1) * (a.N / 2) + (i >> 1) * 16 : i * 16);
     };
+    // 128 bytes of k (block kb) of this CTA's 128 weight rows of tile w.  SwiGLU with I % 16 == 0: one box of
+    // the weights seen as [E][I / 16][2][16][K], whose rows come as 16 gate rows, their 16 up rows, ...
+    auto load_weights = [&](uint32_t dst, uint32_t fb, int kb) {
+        if (!SWIGLU) {
+            tma_load_2d(dst, &tmap_w, fb, kb * STAGE_K, weight_row(w, 0));
+        } else if (a.box) {
+            tma_load_5d(dst, &tmap_w, fb, kb * STAGE_K, 0, 0, (w.n0 + rank * BNC) >> 4, w.e);
+        } else {
+            for (int i = 0; i < 8; ++i) tma_load_2d(dst + i * 16 * STAGE_K, &tmap_w, fb, kb * STAGE_K, weight_row(w, i));
+        }
+    };
+    // Activation rows that this CTA holds of tile t, and the first of them.
+    auto local_rows = [&](const Tile &t) { return (t.rows + STEP - 1) / STEP * STEP / (PAIR ? 2 : 1); };
 
     if (warp == 0) {
-        // -------------------------------------------------------------------- activations (8-bit: weights too)
-        uint32_t it = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; ok && get_tile<BN>(a, off, tiles, t, w); t += gridDim.x) {
-            const int pad = (w.rows + 15) & ~15;
-            // Rows this lane fetches: quads lane and lane + 32 of the tile.  Padding repeats the last
-            // row; an index outside x is replaced by row 0 (the epilogue writes zeros for it).
-            int idx[2][4];
-            if (GATHER) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int r = min(4 * (lane + 32 * q) + j, w.rows - 1);
-                        const int v = __ldg(a.rows + w.r0 + r);
-                        idx[q][j] = (unsigned)v < (unsigned)a.T ? v : 0;
-                    }
-            }
-            const int boxes = (pad + BOX_ROWS - 1) / BOX_ROWS;
-            const uint32_t bytes = (GATHER ? pad : boxes * BOX_ROWS) * STAGE_K + (W4 ? 0 : A_BYTES);
-            for (int kb = 0; kb < kst; ++kb, ++it) {
-                const uint32_t s = it % STAGES, u = it / STAGES;
-                const uint32_t fb = smem_u32(&bar->full[s]);
-                if (lane == 0) {
+        // -------------------------------------------------------------------- TMA: weights (8-bit), ordered rows
+        // The warp runs the loop together and one elected lane issues, so that the operands stay uniform.
+        if (TMA_STAGE) {
+            const bool leader = elect_one();
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = first; ok && get_tile<BN, BR, STEP>(a, off, tiles, t, w); t += stride) {
+                const int boxes = GATHER ? 0 : (local_rows(w) + L::BOX - 1) / L::BOX;
+                const int x0 = w.r0 + rank * local_rows(w);
+                const uint32_t bytes = boxes * L::BOX * STAGE_K + (W4 ? 0 : A_BYTES);
+                for (int kb = 0; kb < kst; ++kb, ++it) {
+                    const uint32_t s = it % STAGES, u = it / STAGES;
+                    const uint32_t fb = smem_u32(&bar->full[s]);
                     ok = wait_parity(smem_u32(&bar->empty[s]), (u & 1) ^ 1, ctl, SITE_PRODUCER);
-                    if (ok) {
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (leader) {
                         mbar_arrive_expect_tx(fb, bytes);
-                        if (!W4) {
-                            if (SWIGLU) {
-                                for (int i = 0; i < 8; ++i)
-                                    tma_load_2d(sA + s * A_BYTES + i * 16 * STAGE_K, &tmap_w, fb, kb * KE,
-                                                weight_row(w, i));
-                            } else {
-                                tma_load_2d(sA + s * A_BYTES, &tmap_w, fb, kb * KE, weight_row(w, 0));
-                            }
-                        }
+                        if (!W4) load_weights(sA + s * A_BYTES, fb, kb);
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d(sB + s * L::B_BYTES + i * L::BOX * STAGE_K, &tmap_x, fb, kb * KE, x0 + i * L::BOX);
                     }
+                    __syncwarp();
                 }
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-                if (!ok) break;
-                const uint32_t dst = sB + s * B_BYTES;
-                if (GATHER) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        if (4 * (lane + 32 * q) < pad)
-                            tma_gather4(dst + 4 * (lane + 32 * q) * STAGE_K, &tmap_x, fb, kb * KE, idx[q][0], idx[q][1],
-                                        idx[q][2], idx[q][3]);
-                } else if (lane < boxes) {
-                    tma_load_2d(dst + lane * BOX_ROWS * STAGE_K, &tmap_x, fb, kb * KE, w.r0 + lane * BOX_ROWS);
-                }
-                __syncwarp();
             }
-        }
-        // Every issued copy lands before the CTA leaves.
-        if (lane == 0) {
+            // Every issued copy lands before the CTA leaves.
             for (uint32_t s = 0; s < STAGES; ++s) {
                 const uint32_t issued = it > s ? (it - s - 1) / STAGES + 1 : 0;
                 if (issued) drain_parity(smem_u32(&bar->full[s]), (issued - 1) & 1, DRAIN_NS, a.status, SITE_DRAIN);
             }
         }
+        __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ---------------------------------------------------------------- MMA issuer
-            uint32_t it = 0, n = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; ok && get_tile<BN>(a, off, tiles, t, w); t += gridDim.x, ++n) {
-                const uint32_t acc = n & 1, u = n >> 1;
-                if (!wait_parity(smem_u32(&bar->acc_empty[acc]), (u & 1) ^ 1, ctl, SITE_MMA)) break;
-                tc_fence_after();
-                const uint32_t d = tmem_base + acc * BR;
-                const uint32_t idesc = idesc_rows<KIND>((w.rows + 15) & ~15);
-                for (int kb = 0; kb < kst; ++kb, ++it) {
-                    const uint32_t s = it % STAGES, us = it / STAGES;
-                    if (!wait_parity(smem_u32(&bar->full[s]), us & 1, ctl, SITE_MMA) ||
-                        (W4 && !wait_parity(smem_u32(&bar->dq_full[s]), us & 1, ctl, SITE_MMA))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < STAGE_K / 32; ++kk)
-                        mma_step<KIND>(d, umma_desc_sw128_kmajor(sA + s * A_BYTES + kk * 32),
-                                       umma_desc_sw128_kmajor(sB + s * B_BYTES + kk * 32), idesc, kb != 0 || kk != 0);
-                    tc_commit(smem_u32(&bar->empty[s]));
-                }
-                if (ok) tc_commit(smem_u32(&bar->acc_full[acc]));
+        // -------------------------------------------------------------------- MMA issuer
+        const bool leader = elect_one();
+        constexpr bool PUT0 = GATHER || W4 || PAIR, PUT1 = GATHER || W4;  // `put` is used in rank 0 / rank 1
+        const uint64_t desc_a = umma_desc_sw128_kmajor(sA), desc_b = umma_desc_sw128_kmajor(sB);
+        uint32_t s = 0, ph = 0, n = 0;
+        bool ok = true;
+        for (int t = first; ok && get_tile<BN, BR, STEP>(a, off, tiles, t, w); t += stride, ++n) {
+            const uint32_t acc = n & 1, d = tmem_base + acc * BR;
+            const uint32_t idesc = idesc_rows<KIND>(PAIR ? 2 * BM : BM, local_rows(w) * (PAIR ? 2 : 1));
+            if (rank == 0) {
+                ok = wait_parity(smem_u32(&bar->acc_empty[acc]), ((n >> 1) & 1) ^ 1, ctl, SITE_MMA);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
             }
-            tc_commit(smem_u32(&bar->drain));
+            for (int kb = 0; kb < kst; ++kb) {
+                ok = (!TMA_STAGE || wait_parity(smem_u32(&bar->full[s]), ph, ctl, SITE_MMA)) &&
+                     (!(rank == 0 ? PUT0 : PUT1) || wait_parity(smem_u32(&bar->put[s]), ph, ctl, SITE_MMA));
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+                if (leader) {
+                    if (rank == 0) {
+                        const uint64_t da = desc_a + s * (A_BYTES >> 4), db = desc_b + s * (L::B_BYTES >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < STAGE_K / 32; ++kk)
+                            mma_step<KIND, PAIR>(d, da + 2 * kk, db + 2 * kk, idesc, kb != 0 || kk != 0);
+                        if (PAIR) tc_commit_pair_both(smem_u32(&bar->empty[s]));
+                        else tc_commit(smem_u32(&bar->empty[s]));
+                    } else {
+                        mbar_arrive_cluster(mapa_shared(smem_u32(&bar->put[s]), 0));
+                    }
+                }
+                __syncwarp();
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+            if (ok && leader && rank == 0) {
+                if (PAIR) tc_commit_pair_both(smem_u32(&bar->acc_full[acc]));
+                else tc_commit(smem_u32(&bar->acc_full[acc]));
+            }
+            __syncwarp();
+        }
+        if (leader && rank == 0) {
+            if (PAIR) tc_commit_pair(smem_u32(&bar->drain));
+            else tc_commit(smem_u32(&bar->drain));
             drain_parity(smem_u32(&bar->drain), 0, DRAIN_NS, a.status, SITE_DRAIN);
         }
         __syncwarp();
     } else if (W4 && warp == 3) {
-        if (lane == 0) {
-            // ---------------------------------------------------------------- packed weight tiles
-            uint32_t it = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; ok && get_tile<BN>(a, off, tiles, t, w); t += gridDim.x) {
-                for (int kb = 0; kb < kst; ++kb, ++it) {
-                    const uint32_t p = it % PSTAGES, u = it / PSTAGES;
-                    if (!wait_parity(smem_u32(&bar->pk_empty[p]), (u & 1) ^ 1, ctl, SITE_PACKED)) {
-                        ok = false;
-                        break;
-                    }
+        // -------------------------------------------------------------------- packed weight tiles
+        const bool leader = elect_one();
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = first; ok && get_tile<BN, BR, STEP>(a, off, tiles, t, w); t += stride) {
+            for (int b = 0; b < packs; ++b, ++it) {
+                const uint32_t p = it % PSTAGES, u = it / PSTAGES;
+                ok = wait_parity(smem_u32(&bar->pk_empty[p]), (u & 1) ^ 1, ctl, SITE_PACKED);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                if (leader) {
                     const uint32_t fb = smem_u32(&bar->pk_full[p]);
                     mbar_arrive_expect_tx(fb, P_BYTES);
-                    if (SWIGLU) {
-                        for (int i = 0; i < 8; ++i)
-                            tma_load_2d(sP + p * P_BYTES + i * 16 * 32, &tmap_w, fb, kb * 32, weight_row(w, i));
-                    } else {
-                        tma_load_2d(sP + p * P_BYTES, &tmap_w, fb, kb * 32, weight_row(w, 0));
-                    }
+                    load_weights(sP + p * P_BYTES, fb, b);
                 }
+                __syncwarp();
             }
-            for (uint32_t p = 0; p < PSTAGES; ++p) {
-                const uint32_t issued = it > p ? (it - p - 1) / PSTAGES + 1 : 0;
-                if (issued) drain_parity(smem_u32(&bar->pk_full[p]), (issued - 1) & 1, DRAIN_NS, a.status, SITE_DRAIN);
-            }
+        }
+        for (uint32_t p = 0; p < PSTAGES; ++p) {
+            const uint32_t issued = it > p ? (it - p - 1) / PSTAGES + 1 : 0;
+            if (issued) drain_parity(smem_u32(&bar->pk_full[p]), (issued - 1) & 1, DRAIN_NS, a.status, SITE_DRAIN);
         }
         __syncwarp();
     } else if (warp >= EPI_WARP0 && warp < EPI_WARP0 + 4) {
@@ -409,7 +467,7 @@ __global__ void __launch_bounds__(Layout<KIND>::THREADS, 1)
         const uint32_t t_row = tmem_base + ((uint32_t)(32 * q) << 16);
         uint32_t n = 0;
         bool ok = true;
-        for (int t = blockIdx.x; get_tile<BN>(a, off, tiles, t, w); t += gridDim.x, ++n) {
+        for (int t = first; get_tile<BN, BR, STEP>(a, off, tiles, t, w); t += stride, ++n) {
             const uint32_t acc = n & 1, u = n >> 1;
             int *src = src_tab + acc * BR;
             float *sxs = sx_tab + acc * BR;
@@ -423,7 +481,7 @@ __global__ void __launch_bounds__(Layout<KIND>::THREADS, 1)
                 if (!W4) sxs[r] = v >= 0 ? __ldg(a.sx + (size_t)v * a.sx_stride) : 0.0f;
             }
             asm volatile("bar.sync 1, 128;" ::: "memory");
-            const int col = w.n0 + (SWIGLU ? 16 * q + (lane & 15) : 32 * q + lane);
+            const int col = w.n0 + rank * BNC + (SWIGLU ? 16 * q + (lane & 15) : 32 * q + lane);
             const bool col_ok = col < a.ldy;
             float sw = 1.0f;
             if (!W4)
@@ -465,108 +523,247 @@ __global__ void __launch_bounds__(Layout<KIND>::THREADS, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bar->acc_empty[acc]));
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&bar->acc_empty[acc]), 0));
+                else mbar_arrive(smem_u32(&bar->acc_empty[acc]));
+            }
         }
-    } else if (W4 && warp >= DQ_WARP0) {
-        // -------------------------------------------------------------------- dequantizers
-        // Thread (row of the tile, half of the stage's 64 codes).
-        const int row = 32 * (warp & 3) + lane, half = (warp - DQ_WARP0) >> 2;
-        const int groups = a.K / a.gs, zwords = (groups + 7) / 8;
+    } else if (GATHER && warp >= L::GA_WARP0 && warp < L::GA_WARP0 + GATHER_WARPS) {
+        // -------------------------------------------------------------------- gathered activations
+        // Thread (16-byte chunk c of a row's 128 bytes, row rr of every 16): cp.async into the 128-byte
+        // swizzle, LAG stages in flight.  Padding repeats the last row; an index outside x reads row 0 (the
+        // epilogue writes zeros for it).
+        constexpr int PASSES = L::SR / 16;
+        const int gt = (int)threadIdx.x - 32 * L::GA_WARP0, c = gt & 7, rr = gt >> 3;
+        const size_t pitch = (size_t)a.K * (W4 ? 2 : 1);
+        const uint32_t dst0 = sB + rr * STAGE_K + ((c ^ (rr & 7)) << 4);
         uint32_t it = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && get_tile<BN>(a, off, tiles, t, w); t += gridDim.x) {
-            const size_t wr = min((size_t)weight_row(w, row >> 4) + (row & 15), (size_t)a.E * a.N - 1);
-            const uint16_t *srow = a.scales + wr * groups;
-            const uint32_t *zrow = a.qzeros + wr * zwords;
-            // A thread's 32 codes of a stage lie in one group; its scale and zero are fetched a stage ahead.
-            auto fetch = [&](int kb, uint32_t &sh, uint32_t &z) {
-                const int g = min((kb * KE + half * 32) / a.gs, groups - 1);
-                sh = __ldg(srow + g);
-                z = (__ldg(zrow + (g >> 3)) >> (4 * (g & 7))) & 0xFu;
-            };
-            uint32_t sh, z;
-            fetch(0, sh, z);
+        auto signal = [&](uint32_t i) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar->put[i % STAGES]));
+        };
+        for (int t = first; ok && get_tile<BN, BR, STEP>(a, off, tiles, t, w); t += stride) {
+            const int mine = local_rows(w);
+            const uint8_t *src[PASSES];
+#pragma unroll
+            for (int j = 0; j < PASSES; ++j) {
+                const int v = __ldg(a.rows + w.r0 + min(rank * mine + 16 * j + rr, w.rows - 1));
+                src[j] = a.x + ((unsigned)v < (unsigned)a.T ? (size_t)v : 0) * pitch;
+            }
             for (int kb = 0; kb < kst; ++kb, ++it) {
-                uint32_t shn = sh, zn = z;
-                if (kb + 1 < kst) fetch(kb + 1, shn, zn);
-                const uint32_t p = it % PSTAGES, up = it / PSTAGES, s = it % STAGES, us = it / STAGES;
-                ok = wait_parity(smem_u32(&bar->pk_full[p]), up & 1, ctl, SITE_DEQUANT);
+                const uint32_t s = it % STAGES, u = it / STAGES;
+                ok = wait_parity(smem_u32(&bar->empty[s]), (u & 1) ^ 1, ctl, SITE_GATHER);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                // 32-byte swizzle: half h of row r lies at h ^ ((r / 4) mod 2).
-                const uint4 q = lds128(sP + p * P_BYTES + row * 32 + ((half ^ ((row >> 2) & 1)) << 4));
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar->pk_empty[p]));
+                const size_t at = (size_t)kb * STAGE_K + c * 16;
+                const bool in = at < pitch;
+#pragma unroll
+                for (int j = 0; j < PASSES; ++j)
+                    if (16 * j < mine)
+                        cp_async16(dst0 + s * L::B_BYTES + 16 * j * STAGE_K, src[j] + (in ? at : 0), in);
+                cp_async_commit();
+                if (it >= LAG) {
+                    cp_async_wait<LAG>();
+                    signal(it - LAG);
+                }
+            }
+        }
+        cp_async_wait<0>();
+        if (ok)
+            for (uint32_t i = it > LAG ? it - LAG : 0; i < it; ++i) signal(i);
+    } else if (W4 && warp >= L::DQ_WARP0) {
+        // -------------------------------------------------------------------- dequantizers
+        // Group g of four warps takes the g-th stage of every packed tile; a thread takes one weight row of it,
+        // 64 codes.
+        constexpr bool BF = KIND == K_W4B;
+        const int row = 32 * (warp & 3) + lane;
+        const uint32_t group = (uint32_t)(warp - L::DQ_WARP0) >> 2;
+        const int lg = 31 - __clz(a.gs), groups = a.K >> lg, zwords = (groups + 7) / 8;
+        const bool vec = groups % 8 == 0;
+        const uint16_t *srow = nullptr;
+        const uint32_t *zrow = nullptr;
+        uint4 ns = {}, cs = {};   // scales and zeros of 8 groups: the next such window's and the current one's
+        uint32_t nz = 0, cz = 0;
+        auto rows_of = [&](const Tile &t) {
+            const size_t wr = min((size_t)weight_row(t, row >> 4) + (row & 15), (size_t)a.E * a.N - 1);
+            srow = a.scales + wr * groups;
+            zrow = a.qzeros + wr * zwords;
+        };
+        auto load = [&](int b) {
+            nz = __ldg(zrow + b);
+            if (vec) {
+                ns = __ldg(reinterpret_cast<const uint4 *>(srow) + b);
+            } else {
+                uint32_t v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = __ldg(srow + min(8 * b + i, groups - 1));
+                ns = make_uint4(v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16));
+            }
+        };
+        uint32_t it0 = 0, pt = 0; // ring positions of the tile's first stage and of the packed tile
+        bool ok = true, have = get_tile<BN, BR, STEP>(a, off, tiles, first, w);
+        if (have) {
+            rows_of(w);
+            load(0);
+        }
+        for (int t = first; ok && have; t += stride, it0 += kst) {
+            // Window 0 of this tile has been loaded; the windows after it, and then the next tile's first,
+            // are requested when the one before them comes into use.
+            int win = 0;
+            cs = ns;
+            cz = nz;
+            bool ahead = false;   // ns, nz hold the next tile's window 0
+            auto request = [&](int b) {
+                if (b < zwords) {
+                    load(b);
+                } else {
+                    have = get_tile<BN, BR, STEP>(a, off, tiles, t + stride, w);
+                    if (have) {
+                        rows_of(w);
+                        load(0);
+                    }
+                    ahead = true;
+                }
+            };
+            request(1);
+            for (int b = 0; b < packs; ++b, ++pt) {
+                const uint32_t p = pt % PSTAGES;
+                const int kb = b * PK + (int)group;
+                ok = wait_parity(smem_u32(&bar->pk_full[p]), (pt / PSTAGES) & 1, ctl, SITE_DEQUANT);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                if (kb >= kst) {  // the tile's depth ends inside the packed tile
+                    if (lane == 0) mbar_arrive(smem_u32(&bar->pk_empty[p]));
+                    continue;
+                }
+                const uint32_t it = it0 + kb, s = it % STAGES, us = it / STAGES;
+                const int g0 = min((kb * KE) >> lg, groups - 1), g1 = min((kb * KE + 32) >> lg, groups - 1);
+                if ((g0 >> 3) != win) {
+                    win = g0 >> 3;
+                    cs = ns;
+                    cz = nz;
+                    request(win + 1);
+                }
+                auto constants = [&](int g) {
+                    const int i = g & 7;
+                    const uint32_t pr = i < 4 ? (i < 2 ? cs.x : cs.y) : (i < 6 ? cs.z : cs.w);
+                    GroupConst<BF> c;
+                    c.set((i & 1) ? pr >> 16 : pr & 0xFFFFu, (cz >> (4 * i)) & 0xFu);
+                    return c;
+                };
+                // 128-byte swizzle: chunk c of row r lies at c ^ (r mod 8).
+                const uint32_t pr = sP + p * P_BYTES + row * STAGE_K;
+                const uint4 q0 = lds128(pr + (((2 * group) ^ (row & 7)) << 4));
+                const uint4 q1 = lds128(pr + (((2 * group + 1) ^ (row & 7)) << 4));
                 ok = wait_parity(smem_u32(&bar->empty[s]), (us & 1) ^ 1, ctl, SITE_DEQUANT);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                const uint32_t s2 = sh | (sh << 16), zc = 0xD400E400u + z * 0x00100001u;
-                const float sf = half_bits_to_float((uint16_t)sh);
-                const uint32_t ws[4] = {q.x, q.y, q.z, q.w};
+                const uint32_t dst = sA + s * A_BYTES + row * STAGE_K;
+                GroupConst<BF> c = constants(g0);
+                const uint32_t w0[4] = {q0.x, q0.y, q0.z, q0.w}, w1[4] = {q1.x, q1.y, q1.z, q1.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    sts128(sA + s * A_BYTES + row * STAGE_K + (((4 * half + j) ^ (row & 7)) << 4),
-                           dequant_word<KIND == K_W4B>(ws[j], zc, s2, sf));
+                for (int j = 0; j < 4; ++j) sts128(dst + ((j ^ (row & 7)) << 4), dequant_word<BF>(w0[j], c));
+                if (g1 != g0) c = constants(g1);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sts128(dst + (((4 + j) ^ (row & 7)) << 4), dequant_word<BF>(w1[j], c));
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar->dq_full[s]));
-                sh = shn;
-                z = zn;
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&bar->pk_empty[p]));
+                    mbar_arrive(smem_u32(&bar->put[s]));
+                }
+            }
+            if (ok && !ahead) {
+                have = get_tile<BN, BR, STEP>(a, off, tiles, t + stride, w);
+                if (have) {
+                    rows_of(w);
+                    load(0);
+                }
             }
         }
     }
 
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // nothing of the other CTA's still arrives here
     if (warp == 2) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, 512);
+        if (PAIR) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+        else tmem_dealloc(tmem_base, TMEM_COLS);
     }
 }
 
-template <Kind KIND, bool GATHER, bool SWIGLU>
-wq_status launch(const CUtensorMap &tx, const CUtensorMap &tw, const Args &a, int grid, cudaStream_t st,
+template <Kind KIND, bool GATHER, bool SWIGLU, bool PAIR>
+wq_status launch(const CUtensorMap &tx, const CUtensorMap &tw, const Args &a, long long most_tiles, cudaStream_t st,
                  const char *who) {
-    auto kern = grouped_gemm_kernel<KIND, GATHER, SWIGLU>;
-    const size_t smem = Layout<KIND>::smem(a.E);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    using L = Layout<KIND, GATHER, PAIR>;
+    auto kern = grouped_gemm_kernel<KIND, GATHER, SWIGLU, PAIR>;
+    const size_t smem = L::smem(a.E);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::smem(MAX_E));
     if (e != cudaSuccess) return fail(WQ_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", who, cudaGetErrorString(e));
-    kern<<<grid, Layout<KIND>::THREADS, smem, st>>>(tx, tw, a);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(L::THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = PAIR ? 2 : 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int units = PAIR ? num_sms() / 2 : num_sms();
+    cfg.gridDim = dim3((unsigned)std::min<long long>(units, most_tiles) * (PAIR ? 2 : 1));
+    e = cudaLaunchKernelEx(&cfg, kern, tx, tw, a);
     if (e != cudaSuccess) return fail(WQ_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return WQ_OK;
 }
 
-// x: [T] rows of K values; w: [E N] rows (of K bytes, or K / 2 packed).
-template <Kind KIND>
-wq_status dispatch(const void *x, const void *w, Args a, bool swiglu, cudaStream_t st, const char *who) {
+// Pair tiles once the experts have rows enough to fill them.
+bool choose_pair(const Args &a) { return (long long)a.R >= 48ll * std::min(a.E, a.R); }
+
+template <Kind KIND, bool PAIR>
+wq_status dispatch(const void *w, Args a, bool swiglu, cudaStream_t st, const char *who) {
     constexpr bool W4 = is_w4(KIND);
     a.status = device_status_word();
     if (!a.status) return WQ_ERR_CUDA;
     a.limit_ns = wait_limit();
     a.ldy = swiglu ? a.N / 2 : a.N;
-    const int bn = swiglu ? BM / 2 : BM;
+    const int bn = (swiglu ? BM / 2 : BM) * (PAIR ? 2 : 1), br = Layout<KIND, false, PAIR>::BR;
     a.nb = (a.ldy + bn - 1) / bn;
-    const long long most = ((long long)std::min(a.E, a.R) + a.R / BR) * a.nb;  // tiles of any offsets
+    const long long most = ((long long)std::min(a.E, a.R) + a.R / br) * a.nb;  // tiles of any offsets
     WQ_REQUIRE(most < INT_MAX / 2, WQ_ERR_UNSUPPORTED, "%s: R (%d) x N (%d) gives too many tiles", who, a.R, a.N);
     const bool gather = a.rows != nullptr;
     CUtensorMap tx, tw;
     const CUtensorMapDataType xt = KIND == K_W4H ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                  : KIND == K_W4B ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const int xb = W4 ? 2 : 1;
-    if (!encode_tmap_2d(&tx, xt, xb, x, (uint64_t)a.K, (uint64_t)a.T, (uint64_t)a.K * xb, STAGE_K / xb,
-                        gather ? 1 : BOX_ROWS, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!encode_tmap_2d(&tx, xt, xb, a.x, (uint64_t)a.K, (uint64_t)a.T, (uint64_t)a.K * xb, STAGE_K / xb,
+                        Layout<KIND, false, PAIR>::BOX,
+                        CU_TENSOR_MAP_SWIZZLE_128B))
         return WQ_ERR_CUDA;
-    const uint64_t wbytes = W4 ? (uint64_t)a.K / 2 : (uint64_t)a.K;
-    if (!encode_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, wbytes, (uint64_t)a.E * a.N, wbytes,
-                        W4 ? 32 : STAGE_K, swiglu ? 16 : BM,
-                        W4 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B))
+    const uint64_t wbytes = W4 ? (uint64_t)a.K / 2 : (uint64_t)a.K, half = (uint64_t)a.N / 2;
+    a.box = swiglu && half % 16 == 0;
+    if (a.box) {
+        const uint64_t dims[5] = {wbytes, 16, 2, half / 16, (uint64_t)a.E};
+        const uint64_t strides[4] = {wbytes, half * wbytes, 16 * wbytes, (uint64_t)a.N * wbytes};
+        const uint32_t box[5] = {STAGE_K, 16, 2, 4, 1};
+        if (!encode_tmap(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, w, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+            return WQ_ERR_CUDA;
+    } else if (!encode_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, wbytes, (uint64_t)a.E * a.N, wbytes, STAGE_K,
+                               swiglu ? 16 : BM, CU_TENSOR_MAP_SWIZZLE_128B)) {
         return WQ_ERR_CUDA;
-    const int grid = (int)std::min<long long>(num_sms(), most);
+    }
     if (gather)
-        return swiglu ? launch<KIND, true, true>(tx, tw, a, grid, st, who)
-                      : launch<KIND, true, false>(tx, tw, a, grid, st, who);
-    return swiglu ? launch<KIND, false, true>(tx, tw, a, grid, st, who)
-                  : launch<KIND, false, false>(tx, tw, a, grid, st, who);
+        return swiglu ? launch<KIND, true, true, PAIR>(tx, tw, a, most, st, who)
+                      : launch<KIND, true, false, PAIR>(tx, tw, a, most, st, who);
+    return swiglu ? launch<KIND, false, true, PAIR>(tx, tw, a, most, st, who)
+                  : launch<KIND, false, false, PAIR>(tx, tw, a, most, st, who);
+}
+
+template <Kind KIND>
+wq_status run(const void *x, const void *w, Args a, bool swiglu, cudaStream_t st, const char *who) {
+    a.x = static_cast<const uint8_t *>(x);
+    return choose_pair(a) ? dispatch<KIND, true>(w, a, swiglu, st, who) : dispatch<KIND, false>(w, a, swiglu, st, who);
 }
 
 // Checks that every grouped product makes of its sizes.
@@ -605,7 +802,7 @@ wq_status w4_entry(const uint16_t *x, int T, const int32_t *rows, const int32_t 
     a.qzeros = qzeros;
     a.y = y;
     a.T = T; a.R = R; a.E = E; a.N = N; a.K = K; a.gs = group_size;
-    return dispatch<KIND>(x, qweight, a, swiglu != 0, as_stream(stream), who);
+    return run<KIND>(x, qweight, a, swiglu != 0, as_stream(stream), who);
 }
 
 template <Kind KIND>
@@ -631,7 +828,7 @@ wq_status w8_entry(const void *xq, const float *sx, int sx_per_row, int T, const
     a.sw_per_row = sw_per_row != 0;
     a.y = y;
     a.T = T; a.R = R; a.E = E; a.N = N; a.K = K;
-    return dispatch<KIND>(xq, wq_, a, swiglu != 0, as_stream(stream), who);
+    return run<KIND>(xq, wq_, a, swiglu != 0, as_stream(stream), who);
 }
 
 }  // namespace

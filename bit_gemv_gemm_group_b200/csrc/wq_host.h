@@ -48,6 +48,11 @@ bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, int elem_bytes,
                     uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
                     CUtensorMapSwizzle swizzle);
 
+// The same for an array of up to 5 dimensions: dims and box from the innermost one, strides (bytes) of
+// dimensions 1 .. rank - 1.
+bool encode_tmap(CUtensorMap *map, CUtensorMapDataType dtype, int rank, const void *base, const uint64_t *dims,
+                 const uint64_t *strides, const uint32_t *box, CUtensorMapSwizzle swizzle);
+
 }  // namespace wq
 
 #define WQ_REQUIRE(cond, status, ...)                     \
