@@ -11,7 +11,6 @@ library's ``uint32`` words) and fp16 as ``torch.float16``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -520,28 +519,40 @@ def awq(w: torch.Tensor, x: torch.Tensor, grid=None, group_size: int = 128, stre
 # --------------------------------------------------------------------------
 # mixture-of-experts layers
 # --------------------------------------------------------------------------
-_HERE = contextlib.nullcontext()
 _DTYPE = {torch.float32: WQ_F32, torch.float16: WQ_F16, torch.bfloat16: WQ_BF16}
 
 
-def _on(t: torch.Tensor, stream):
-    """Context in which outputs and scratch of a call on `t` are allocated and its kernels launched: t's device,
-    and `stream` where one is given (so that scratch freed at the end of the call is not reused before it is done)."""
-    if stream is not None:
-        if stream.device != t.device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
-        return torch.cuda.stream(stream)
-    return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+def _moe_stream(t: torch.Tensor, stream) -> int:
+    """Handle of the stream that a call on `t` runs on: `stream`, or the current one of t's device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.device.index)
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+    return stream.cuda_stream
 
 
-def _with(first: torch.Tensor, t: torch.Tensor, name: str, dtypes, shape) -> torch.Tensor:
-    """`t` checked like `_cuda`, to have `shape` and to be on the device of `first`."""
-    _cuda(t, name, dtypes)
-    if tuple(t.shape) != tuple(shape):
+def _elsewhere(t: torch.Tensor, stream) -> bool:
+    """Whether the call has to enter another device or stream first: outputs and scratch are allocated there, so that
+    what is freed at the end of the call is not reused before its kernels are done."""
+    return stream is not None or t.device.index != torch._C._cuda_getDevice()
+
+
+def _enter(t: torch.Tensor, stream):
+    if stream is None:
+        return torch.cuda.device(t.device)
+    _moe_stream(t, stream)
+    return torch.cuda.stream(stream)
+
+
+def _with(first: torch.Tensor, t: torch.Tensor, name: str, dtype, shape) -> None:
+    """Checks that `t` is a contiguous tensor of this dtype and shape on the device of `first`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() \
+            and t.device == first.device:
+        return
+    _cuda(t, name, (dtype,))
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != first.device:
-        raise ValueError(f"{name} is on {t.device}, expected {first.device}")
-    return t
+    raise ValueError(f"{name} is on {t.device}, expected {first.device}")
 
 
 def moe_route_workspace_bytes(T: int, E: int) -> int:
@@ -556,41 +567,49 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, worksp
     rows int32 [T * k], slots int32 [T, k]).  Equal logits go to the lowest expert; NaN and -inf are never chosen
     (id -1, weight 0, slot -1 where nothing is left).  Expert e's sorted rows are offsets[e]:offsets[e + 1]."""
     _cuda(logits, "logits", (torch.float32, torch.float16, torch.bfloat16), 2)
+    if _elsewhere(logits, stream):
+        with _enter(logits, stream):
+            return moe_route(logits, top_k, renormalize, workspace)
     T, E = logits.shape
     k = int(top_k)
-    with _on(logits, stream):
-        ids = _empty((T, max(k, 0)), torch.int32, logits)
-        weights = _empty((T, max(k, 0)), torch.float32, logits)
-        offsets = _empty((E + 1,), torch.int32, logits)
-        rows = _empty((T * max(k, 0),), torch.int32, logits)
-        slots = _empty((T, max(k, 0)), torch.int32, logits)
-        need = moe_route_workspace_bytes(T, E)
-        if workspace is None:
-            workspace = _empty((need,), torch.uint8, logits) if need else None
-        else:
-            _cuda(workspace, "workspace", (torch.uint8,), 1)
-            if workspace.numel() < need or workspace.device != logits.device:
-                raise ValueError(f"workspace must hold {need} bytes on {logits.device}")
-        _check(lib.wq_moe_route(_ptr(logits), _DTYPE[logits.dtype], T, E, k, int(bool(renormalize)), _ptr(ids),
-                                _ptr(weights), _ptr(offsets), _ptr(rows), _ptr(slots), _ptr(workspace),
-                                _P(_stream())), "wq_moe_route")
+    pairs = T * max(k, 0)
+    new = logits.new_empty
+    ids, slots = new((2, T, max(k, 0)), dtype=torch.int32).unbind(0) if pairs % 4 == 0 else \
+        (new((T, max(k, 0)), dtype=torch.int32), new((T, max(k, 0)), dtype=torch.int32))  # 16-byte aligned each
+    weights = new((T, max(k, 0)), dtype=torch.float32)
+    offsets = new((E + 1,), dtype=torch.int32)
+    rows = new((pairs,), dtype=torch.int32)
+    need = lib.wq_moe_route_workspace_bytes(T, E)
+    if workspace is None:
+        workspace = new((need,), dtype=torch.uint8) if need else None
+    else:
+        _cuda(workspace, "workspace", (torch.uint8,), 1)
+        if workspace.numel() < need or workspace.device != logits.device:
+            raise ValueError(f"workspace must hold {need} bytes on {logits.device}")
+    status = lib.wq_moe_route(logits.data_ptr(), _DTYPE[logits.dtype], T, E, k, 1 if renormalize else 0,
+                              ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
+                              slots.data_ptr(), None if workspace is None else workspace.data_ptr(),
+                              _moe_stream(logits, None))
+    if status:
+        _check(status, "wq_moe_route")
     return ids, weights, offsets, rows, slots
 
 
-def _grouped_rows(x, offsets, rows, E):
-    """(T, R) of a grouped product: rows of x, sorted rows."""
-    _with(x, offsets, "offsets", (torch.int32,), (E + 1,))
-    if rows is None:
-        return x.shape[0], x.shape[0]
-    _with(x, rows, "rows", (torch.int32,), (rows.numel(),))
-    return x.shape[0], rows.numel()
-
-
-def _grouped_out(x, out, R, N, swiglu, dtype):
+def _grouped(x, offsets, rows, E, N, swiglu, out, dtype):
+    """(T, R, pointer of rows, output) of a grouped product."""
+    T = R = x.shape[0]
+    _with(x, offsets, "offsets", torch.int32, (E + 1,))
+    if rows is not None:
+        R = rows.numel()
+        _with(x, rows, "rows", torch.int32, (R,))
     if swiglu and N % 2:
         raise ValueError("the weights must have an even number of rows with swiglu")
-    shape = (R, N // 2 if swiglu else N)
-    return _empty(shape, dtype, x) if out is None else _with(x, out, "out", (dtype,), shape)
+    cols = N // 2 if swiglu else N
+    if out is None:
+        out = x.new_empty((R, cols), dtype=dtype)
+    else:
+        _with(x, out, "out", dtype, (R, cols))
+    return T, R, None if rows is None else rows.data_ptr(), out
 
 
 def grouped_gemm_w4a16(x, qweight, scales, qzeros, offsets, rows=None, group_size: int = 128, swiglu: bool = False,
@@ -602,22 +621,25 @@ def grouped_gemm_w4a16(x, qweight, scales, qzeros, offsets, rows=None, group_siz
     None: the rows of x are sorted already).  swiglu: N = 2 I, y = silu(gate) * up of rows i and I + i.
     -> [R, N or I] in x's dtype; rows outside the experts' ranges are not written."""
     _cuda(x, "x", (torch.float16, torch.bfloat16), 2)
+    if _elsewhere(x, stream):
+        with _enter(x, stream):
+            return grouped_gemm_w4a16(x, qweight, scales, qzeros, offsets, rows, group_size, swiglu, out)
     _cuda(qweight, "qweight", (torch.int32,), 3)
     E, N, words = qweight.shape
     K = x.shape[1]
     if words * 8 != K or group_size <= 0 or K % group_size:
         raise ValueError("qweight must be [E, N, K/8] and K a multiple of group_size")
-    _with(x, qweight, "qweight", (torch.int32,), (E, N, K // 8))
-    _with(x, scales, "scales", (torch.float16,), (E, N, K // group_size))
-    _with(x, qzeros, "qzeros", (torch.int32,), (E, N, (K // group_size + 7) // 8))
-    T, R = _grouped_rows(x, offsets, rows, E)
-    bf16 = x.dtype == torch.bfloat16
-    fn = lib.wq_grouped_gemm_w4a16_bf16 if bf16 else lib.wq_grouped_gemm_w4a16
-    with _on(x, stream):
-        y = _grouped_out(x, out, R, N, swiglu, x.dtype)
-        _check(fn(_ptr(x), T, _ptr(rows), _ptr(offsets), R, _ptr(qweight), _ptr(scales), _ptr(qzeros), E, N, K,
-                  group_size, int(bool(swiglu)), _ptr(y), _P(_stream())),
-               "wq_grouped_gemm_w4a16_bf16" if bf16 else "wq_grouped_gemm_w4a16")
+    groups = K // group_size
+    _with(x, qweight, "qweight", torch.int32, (E, N, words))
+    _with(x, scales, "scales", torch.float16, (E, N, groups))
+    _with(x, qzeros, "qzeros", torch.int32, (E, N, (groups + 7) // 8))
+    T, R, rp, y = _grouped(x, offsets, rows, E, N, swiglu, out, x.dtype)
+    bf16 = x.dtype is torch.bfloat16
+    status = (lib.wq_grouped_gemm_w4a16_bf16 if bf16 else lib.wq_grouped_gemm_w4a16)(
+        x.data_ptr(), T, rp, offsets.data_ptr(), R, qweight.data_ptr(), scales.data_ptr(), qzeros.data_ptr(), E, N, K,
+        group_size, 1 if swiglu else 0, y.data_ptr(), _moe_stream(x, None))
+    if status:
+        _check(status, "wq_grouped_gemm_w4a16_bf16" if bf16 else "wq_grouped_gemm_w4a16")
     return y
 
 
@@ -627,16 +649,19 @@ def grouped_gemm_w8a8(xq, sx, wq, sw, offsets, rows=None, swiglu: bool = False, 
     xq int8 [T, K], sx fp32 [T] (quantize_int8_per_token); wq int8 [E, N, K], sw fp32 [E, N] (stacked
     quantize_int8_per_channel); offsets, rows, swiglu and the result as for grouped_gemm_w4a16 (fp16)."""
     _cuda(xq, "xq", (torch.int8,), 2)
+    if _elsewhere(xq, stream):
+        with _enter(xq, stream):
+            return grouped_gemm_w8a8(xq, sx, wq, sw, offsets, rows, swiglu, out)
     _cuda(wq, "wq", (torch.int8,), 3)
     E, N, K = wq.shape
-    T, R = _grouped_rows(xq, offsets, rows, E)
-    _with(xq, wq, "wq", (torch.int8,), (E, N, xq.shape[1]))
-    _with(xq, sx, "sx", (torch.float32,), (T,))
-    _with(xq, sw, "sw", (torch.float32,), (E, N))
-    with _on(xq, stream):
-        y = _grouped_out(xq, out, R, N, swiglu, torch.float16)
-        _check(lib.wq_grouped_gemm_w8a8(_ptr(xq), _ptr(sx), T, _ptr(rows), _ptr(offsets), R, _ptr(wq), _ptr(sw), E, N,
-                                        K, int(bool(swiglu)), _ptr(y), _P(_stream())), "wq_grouped_gemm_w8a8")
+    _with(xq, wq, "wq", torch.int8, (E, N, xq.shape[1]))
+    _with(xq, sx, "sx", torch.float32, (xq.shape[0],))
+    _with(xq, sw, "sw", torch.float32, (E, N))
+    T, R, rp, y = _grouped(xq, offsets, rows, E, N, swiglu, out, torch.float16)
+    status = lib.wq_grouped_gemm_w8a8(xq.data_ptr(), sx.data_ptr(), T, rp, offsets.data_ptr(), R, wq.data_ptr(),
+                                      sw.data_ptr(), E, N, K, 1 if swiglu else 0, y.data_ptr(), _moe_stream(xq, None))
+    if status:
+        _check(status, "wq_grouped_gemm_w8a8")
     return y
 
 
@@ -644,19 +669,22 @@ def grouped_gemm_fp8(xq, sx, wq, sw, offsets, rows=None, swiglu: bool = False, o
     """Expert products in FP8 E4M3 (codes as uint8): as grouped_gemm_w8a8, with sx fp32 [T] or [1] and sw fp32
     [E, N] or [E] (per token or per tensor; per channel or per expert)."""
     _cuda(xq, "xq", (torch.uint8,), 2)
+    if _elsewhere(xq, stream):
+        with _enter(xq, stream):
+            return grouped_gemm_fp8(xq, sx, wq, sw, offsets, rows, swiglu, out)
     _cuda(wq, "wq", (torch.uint8,), 3)
     E, N, K = wq.shape
-    T, R = _grouped_rows(xq, offsets, rows, E)
-    _with(xq, wq, "wq", (torch.uint8,), (E, N, xq.shape[1]))
-    if tuple(sx.shape) not in ((T,), (1,)) or tuple(sw.shape) not in ((E, N), (E,)):
+    _with(xq, wq, "wq", torch.uint8, (E, N, xq.shape[1]))
+    if sx.shape not in ((xq.shape[0],), (1,)) or sw.shape not in ((E, N), (E,)):
         raise ValueError("shape mismatch: sx must be [T] or [1], sw [E, N] or [E]")
-    _with(xq, sx, "sx", (torch.float32,), sx.shape)
-    _with(xq, sw, "sw", (torch.float32,), sw.shape)
-    with _on(xq, stream):
-        y = _grouped_out(xq, out, R, N, swiglu, torch.float16)
-        _check(lib.wq_grouped_gemm_fp8(_ptr(xq), _ptr(sx), int(sx.numel() == T), T, _ptr(rows), _ptr(offsets), R,
-                                       _ptr(wq), _ptr(sw), int(sw.dim() == 2), E, N, K, int(bool(swiglu)), _ptr(y),
-                                       _P(_stream())), "wq_grouped_gemm_fp8")
+    _with(xq, sx, "sx", torch.float32, sx.shape)
+    _with(xq, sw, "sw", torch.float32, sw.shape)
+    T, R, rp, y = _grouped(xq, offsets, rows, E, N, swiglu, out, torch.float16)
+    status = lib.wq_grouped_gemm_fp8(xq.data_ptr(), sx.data_ptr(), 1 if sx.numel() == T else 0, T, rp,
+                                     offsets.data_ptr(), R, wq.data_ptr(), sw.data_ptr(), 1 if sw.dim() == 2 else 0, E,
+                                     N, K, 1 if swiglu else 0, y.data_ptr(), _moe_stream(xq, None))
+    if status:
+        _check(status, "wq_grouped_gemm_fp8")
     return y
 
 
@@ -665,23 +693,30 @@ def moe_combine(y, weights, slots, out=None, stream=None):
 
     y [R, N] fp16 or bf16; weights fp32 [T, k] and slots int32 [T, k] as moe_route gives them."""
     _cuda(y, "y", (torch.float16, torch.bfloat16), 2)
+    if _elsewhere(y, stream):
+        with _enter(y, stream):
+            return moe_combine(y, weights, slots, out)
     _cuda(slots, "slots", (torch.int32,), 2)
     T, k = slots.shape
     R, N = y.shape
-    _with(y, slots, "slots", (torch.int32,), (T, k))
-    _with(y, weights, "weights", (torch.float32,), (T, k))
-    with _on(y, stream):
-        o = _empty((T, N), y.dtype, y) if out is None else _with(y, out, "out", (y.dtype,), (T, N))
-        _check(lib.wq_moe_combine(_ptr(y), _DTYPE[y.dtype], R, _ptr(weights), _ptr(slots), T, k, N, _ptr(o),
-                                  _P(_stream())), "wq_moe_combine")
-    return o
+    _with(y, slots, "slots", torch.int32, (T, k))
+    _with(y, weights, "weights", torch.float32, (T, k))
+    if out is None:
+        out = y.new_empty((T, N))
+    else:
+        _with(y, out, "out", y.dtype, (T, N))
+    status = lib.wq_moe_combine(y.data_ptr(), _DTYPE[y.dtype], R, weights.data_ptr(), slots.data_ptr(), T, k, N,
+                                out.data_ptr(), _moe_stream(y, None))
+    if status:
+        _check(status, "wq_moe_combine")
+    return out
 
 
 def moe_mlp_w4a16(x, logits, gate_up, down, top_k: int, group_size: int = 128, renormalize: bool = True, stream=None):
     """A mixture-of-experts feed-forward layer with INT4 experts: router, gate and up projection with SwiGLU, down
     projection, combine.  x [T, K] fp16 or bf16, logits [T, E]; gate_up and down are (qweight, scales, qzeros) stacked
     over the experts, [E, 2 I, ...] over K and [E, N, ...] over I.  -> [T, N] in x's dtype."""
-    with _on(x, stream):
+    with _enter(x, stream):
         _, weights, offsets, rows, slots = moe_route(logits, top_k, renormalize)
         h = grouped_gemm_w4a16(x, *gate_up, offsets, rows, group_size, swiglu=True)
         y = grouped_gemm_w4a16(h, *down, offsets, None, group_size)
@@ -691,7 +726,7 @@ def moe_mlp_w4a16(x, logits, gate_up, down, top_k: int, group_size: int = 128, r
 def moe_mlp_w8a8(x, logits, gate_up, down, top_k: int, renormalize: bool = True, stream=None):
     """The same layer with INT8 experts: x fp16 [T, K] and the SwiGLU outputs are quantized per token; gate_up and
     down are (wq, sw) stacked over the experts.  -> fp16 [T, N]."""
-    with _on(x, stream):
+    with _enter(x, stream):
         _, weights, offsets, rows, slots = moe_route(logits, top_k, renormalize)
         xq, sx = quantize_int8_per_token(x)
         h = grouped_gemm_w8a8(xq, sx, *gate_up, offsets, rows, swiglu=True)
