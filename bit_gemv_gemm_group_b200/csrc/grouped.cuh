@@ -1,0 +1,128 @@
+// Shared by the kernels of the expert products: arguments, the tile list that every CTA derives from the
+// offsets in device memory, and small device helpers.
+#pragma once
+
+#include "sm100.cuh"
+#include "wq_device.cuh"
+#include "wq_host.h"
+
+namespace wq {
+namespace grouped {
+
+constexpr int BM = 128;                // weight rows of a CTA's share of a tile (TMEM lanes)
+constexpr int MAX_E = 512;
+constexpr uint64_t DRAIN_NS = 2000000000ull;
+
+struct Args {
+    const uint8_t *x;                // [T] rows
+    const int32_t *offsets, *rows;   // rows null: row p of x itself
+    const float *sx, *sw;
+    int sx_stride, sw_per_row;
+    const uint16_t *scales;          // INT4: fp16 [E][N][K/gs]
+    const uint32_t *qzeros;
+    uint16_t *y;
+    int T, R, E, N, K, gs;           // T: rows of x, R: grouped rows
+    int nb;                          // weight-row blocks per expert
+    int box;                         // SwiGLU: the weight map is the 5-D one (see load_weights)
+    int ldy;                         // columns of y (N, or N / 2 with SwiGLU)
+    unsigned int *status;
+    uint64_t limit_ns;
+};
+
+struct Tile {
+    int e, n0;        // expert, first output column of the tile
+    int r0, rows;     // first grouped row, number of rows
+};
+
+// Offsets clamped to [0, R] and made non-decreasing (a valid array is unchanged), and the exclusive
+// prefix of the experts' tile counts; by one warp.
+template <int BR>
+__device__ __forceinline__ void build_table(const Args &a, int *off, int *tiles, int lane) {
+    int high = 0;
+    for (int i0 = 0; i0 <= a.E; i0 += 32) {
+        int v = i0 + lane <= a.E ? min(max(__ldg(a.offsets + i0 + lane), 0), a.R) : 0;
+        v = max(v, high);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) v = max(v, __shfl_up_sync(0xffffffffu, v, o));
+        if (i0 + lane <= a.E) off[i0 + lane] = v;
+        high = __shfl_sync(0xffffffffu, v, 31);
+    }
+    __syncwarp();
+    int run = 0;
+    for (int i0 = 0; i0 < a.E; i0 += 32) {
+        const int v = i0 + lane < a.E ? (off[i0 + lane + 1] - off[i0 + lane] + BR - 1) / BR * a.nb : 0;
+        int s = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += n;
+        }
+        if (i0 + lane < a.E) tiles[i0 + lane] = run + s - v;
+        run += __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (lane == 0) tiles[a.E] = run;
+}
+
+// Tile t of the list; false past its end.  BN: output columns per tile, BR and STEP: most rows of a block
+// and what its length is rounded up to.
+template <int BN, int BR, int STEP>
+__device__ __forceinline__ bool get_tile(const Args &a, const int *off, const int *tiles, int t, Tile &w) {
+    if (t >= tiles[a.E]) return false;
+    int lo = 0, hi = a.E;  // the expert e with tiles[e] <= t < tiles[e + 1]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (tiles[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    const int first = off[lo], n = off[lo + 1] - first, rb = (n + BR - 1) / BR;
+    const int per = ((n + rb - 1) / rb + STEP - 1) / STEP * STEP;
+    const int local = t - tiles[lo], b = local % rb;
+    w.e = lo;
+    w.n0 = (local / rb) * BN;
+    w.r0 = first + b * per;
+    w.rows = min(per, n - b * per);
+    return true;
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+// silu(g) u.  The fast exponential and division are off by a few fp32 units, far below the 16-bit
+// rounding that follows.
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+// Map of the stacked weights for tiles of 128 rows x 128 bytes with the 128-byte swizzle (row_bytes: bytes of
+// a weight row).  SwiGLU with I % 16 == 0: the 5-D view [E][I / 16][2][16][row] (a.box), whose box of
+// 4 x 2 x 16 rows is 16 gate rows, their 16 up rows, and so on; otherwise boxes of 16 rows.
+bool encode_weights(CUtensorMap *map, const void *w, uint64_t row_bytes, Args &a, bool swiglu);
+
+// INT4 weights and at most a few dozen rows per expert (grouped_few.cu); `bf16`: type of x and y.
+wq_status few_rows_w4(const void *w, Args a, bool bf16, bool swiglu, cudaStream_t st, const char *who);
+
+}  // namespace grouped
+}  // namespace wq

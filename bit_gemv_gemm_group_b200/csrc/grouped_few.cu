@@ -1,0 +1,582 @@
+// Expert products with INT4 weights for few rows per expert (decode batches): the same products as
+// grouped_gemm.cu's kernel, whose tiles these are, organised around the stream of packed weights.
+//
+//   y[p][n] = sum_j s[n][j] * ( sum_{k in group j} (q[n][k] - z[n][j]) x[rows[p]][k] )
+//
+// With 16 or 32 activation rows a weight takes part in so few products that turning it into an fp16 value
+// s (q - z) would cost more than the tensor cores' work on it.  So the MMA's operand is q - z itself, an
+// integer of 5 bits that fp16 and bf16 hold exactly, every group of codes has an accumulator of its own in
+// tensor memory, and the group's scale multiplies the 128 x rows sums in fp32 when the group is done: no
+// weight is rounded, and a scale costs one fma per row of x instead of one product per code.
+//
+// Persistent CTA, one per SM; a tile is 128 weight rows times up to 32 rows of one expert, and the S CTAs
+// of a cluster share a tile's depth, so that the last round of tiles is short:
+//   warp 0       TMA: 128 rows x 128 bytes (256 codes) of packed weights into a deep ring
+//   warp 1       an elected thread issues tcgen05.mma (A from tensor memory, 128 codes per stage)
+//   warps 2, 3   (2 allocates tensor memory) rows of x by cp.async, 128-byte swizzle
+//   warps 4-7    scale: each group's accumulator, times the scale of the lane's weight row, into registers;
+//                at the end of a tile the cluster's parts meet in the first CTA's shared memory, which
+//                applies SwiGLU, rounds and stores
+//   warps 8-23   four groups of four warps: codes -> q - z into tensor memory, every fourth stage each
+#include "grouped.cuh"
+
+#include <algorithm>
+#include <climits>
+
+namespace wq {
+namespace grouped {
+namespace {
+
+using namespace sm100;
+
+constexpr int BR = 32;                      // rows of a tile, at most (16 or 32)
+constexpr int SK = 128;                     // codes per stage
+constexpr int A_STAGES = 4, X_STAGES = 6, P_SLOTS = 7, ACCS = 8, LAG = 3;
+constexpr uint32_t X_ATOM = BR * 128, X_BYTES = 2 * X_ATOM;   // 64 values a row and atom
+constexpr uint32_t P_BYTES = BM * 128;      // 256 codes of 128 rows: two stages
+constexpr uint32_t A_COLS = SK / 2;         // tensor memory columns of a stage
+constexpr uint32_t A_COL0 = ACCS * BR;      // after the accumulators
+constexpr int THREADS = 768, SCALE_WARP0 = 4, DQ_WARP0 = 8;
+constexpr int MAX_SPLIT = 4;
+constexpr uint32_t OFF_X = P_SLOTS * P_BYTES;
+constexpr uint32_t OFF_RED = OFF_X + X_STAGES * X_BYTES;      // not used when the tile is not split
+constexpr uint32_t RED_BYTES = BM * BR * 4;                   // one CTA's part of a tile
+constexpr unsigned SITE_PACKED = 0x2001, SITE_MMA = 0x2002, SITE_GATHER = 0x2004, SITE_SCALE = 0x2008,
+                   SITE_DEQUANT = 0x2010, SITE_DRAIN = 0x2020, SITE_SPLIT = 0x2040;
+static_assert(A_COL0 + A_STAGES * A_COLS <= 512, "tensor memory");
+
+struct Bars {
+    uint64_t pk_full[P_SLOTS], pk_empty[P_SLOTS];
+    uint64_t x_full[X_STAGES], x_empty[X_STAGES];
+    uint64_t a_full[A_STAGES], a_empty[A_STAGES];
+    uint64_t acc_full[ACCS], acc_empty[ACCS];
+    uint64_t red_full[4], red_free[4];      // per scale warp: the other CTAs' parts are here / may be sent
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+constexpr size_t smem_bytes(int split, int E) {
+    return 1024 + OFF_RED + (size_t)(split - 1) * RED_BYTES + 1024 + 2 * (size_t)(E + 1) * 4;
+}
+
+static_assert(smem_bytes(MAX_SPLIT, MAX_E) <= 232448 && sizeof(Bars) <= 1024 && X_STAGES > LAG, "shared memory");
+
+// q - z of the 8 codes of a word, in k order, as fp16 or bf16 pairs.  zc: the fp16 pair -(1024 + z),
+// -(64 + z), or the bf16 pair -(128 + z) twice (see dequant_word in grouped_gemm.cu).
+template <bool BF>
+__device__ __forceinline__ void code_word(uint32_t w, uint32_t zc, uint32_t *o) {
+    const uint32_t w4 = w >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (BF) {
+            const uint32_t h = (prmt(w, w4, 0x4400u + 0x1111u * i) & 0x000F000Fu) | 0x43004300u;
+            asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(h), "r"(zc));
+        } else {
+            const uint32_t h = (prmt(w, 0u, 0x4040u + 0x0101u * i) & 0x00F0000Fu) | 0x64006400u;
+            o[i] = hfma2(h, 0x2C003C00u, zc);
+        }
+    }
+}
+
+template <bool BF>
+__device__ __forceinline__ uint16_t round_bits(float v) {
+    return BF ? float_to_bf16_bits_rn(v) : float_to_half_bits_rn(v);
+}
+
+// The part of a tile's depth that CTA `rank` of `split` takes: stages [s0, s1), in whole packed tiles.
+struct Depth {
+    int s0, s1;
+    __device__ __forceinline__ Depth(int K, int rank, int split) {
+        const int st = (K + SK - 1) / SK, packs = (st + 1) / 2;
+        s0 = 2 * (int)((long long)packs * rank / split);
+        s1 = min(st, 2 * (int)((long long)packs * (rank + 1) / split));
+    }
+};
+
+template <bool BF, bool SWIGLU>
+__global__ void __launch_bounds__(THREADS, 1)
+    few_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const Args a, int split) {
+    constexpr int BN = SWIGLU ? BM / 2 : BM;   // output columns per tile
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t off_bar = OFF_RED + (split - 1) * RED_BYTES;
+    Bars *bar = reinterpret_cast<Bars *>(base + off_bar);
+    int *off = reinterpret_cast<int *>(base + off_bar + 1024), *tiles = off + a.E + 1;
+    const uint32_t sP = smem_u32(base), sX = smem_u32(base + OFF_X), sR = smem_u32(base + OFF_RED);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = split > 1 ? (int)cluster_ctarank() : 0;
+    const int first = (int)blockIdx.x / split, stride = (int)gridDim.x / split;
+    const Depth dep(a.K, rank, split);
+    const int lg = 31 - __clz(a.gs), groups = a.K >> lg, zwords = (groups + 7) / 8;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < P_SLOTS; ++i) {
+            mbar_init(smem_u32(&bar->pk_full[i]), 1);
+            mbar_init(smem_u32(&bar->pk_empty[i]), 8);
+        }
+        for (int i = 0; i < X_STAGES; ++i) {
+            mbar_init(smem_u32(&bar->x_full[i]), 2);
+            mbar_init(smem_u32(&bar->x_empty[i]), 1);
+        }
+        for (int i = 0; i < A_STAGES; ++i) {
+            mbar_init(smem_u32(&bar->a_full[i]), 4);
+            mbar_init(smem_u32(&bar->a_empty[i]), 1);
+        }
+        for (int i = 0; i < ACCS; ++i) {
+            mbar_init(smem_u32(&bar->acc_full[i]), 1);
+            mbar_init(smem_u32(&bar->acc_empty[i]), 4);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(smem_u32(&bar->red_full[i]), max(1, split - 1));
+            mbar_init(smem_u32(&bar->red_free[i]), 1);
+        }
+        mbar_init(smem_u32(&bar->drain), 1);
+        bar->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) prefetch_tmap(&tmap_w);
+    if (warp == 1) build_table<BR>(a, off, tiles, lane);
+    if (warp == 2) {
+        tmem_alloc(smem_u32(&bar->tmem_base), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (split > 1) cluster_sync();  // every CTA's barriers are set up before another arrives on them
+    tc_fence_after();
+    const uint32_t tmem = bar->tmem_base;
+    const WaitCtl ctl{&bar->abort, a.status, a.limit_ns};
+    Tile w;
+
+    // First weight row (of the stacked [E N] rows) of lane group i (16 lanes) of tile t.
+    auto weight_row = [&](const Tile &t, int i) {
+        return t.e * a.N + t.n0 + (SWIGLU ? (i & 1) * (a.N / 2) + (i >> 1) * 16 : i * 16);
+    };
+
+    if (warp == 0) {
+        // -------------------------------------------------------------------- packed weights
+        const bool leader = elect_one();
+        uint32_t p = 0, ph = 1, it = 0;
+        bool ok = true;
+        for (int t = first; ok && get_tile<BN, BR, 16>(a, off, tiles, t, w); t += stride) {
+            for (int sb = dep.s0; sb < dep.s1; sb += 2, ++it) {
+                ok = wait_parity(smem_u32(&bar->pk_empty[p]), ph, ctl, SITE_PACKED);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                if (leader) {
+                    const uint32_t fb = smem_u32(&bar->pk_full[p]), dst = sP + p * P_BYTES;
+                    mbar_arrive_expect_tx(fb, P_BYTES);
+                    if (!SWIGLU) {
+                        tma_load_2d(dst, &tmap_w, fb, sb * 64, weight_row(w, 0));
+                    } else if (a.box) {
+                        tma_load_5d(dst, &tmap_w, fb, sb * 64, 0, 0, w.n0 >> 4, w.e);
+                    } else {
+                        for (int i = 0; i < 8; ++i)
+                            tma_load_2d(dst + i * 16 * 128, &tmap_w, fb, sb * 64, weight_row(w, i));
+                    }
+                }
+                __syncwarp();
+                if (++p == P_SLOTS) {
+                    p = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        for (uint32_t i = 0; i < P_SLOTS; ++i) {  // every issued copy lands before the CTA leaves
+            const uint32_t issued = it > i ? (it - i - 1) / P_SLOTS + 1 : 0;
+            if (issued) drain_parity(smem_u32(&bar->pk_full[i]), (issued - 1) & 1, DRAIN_NS, a.status, SITE_DRAIN);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // -------------------------------------------------------------------- MMA issuer
+        const bool leader = elect_one();
+        const uint64_t desc_x = umma_desc_sw128_kmajor(sX);
+        const int gsteps = a.gs / 16;   // MMAs (16 codes) per group
+        uint32_t as = 0, ap = 0, xs = 0, xp = 0, cs = 0, cp = 1;  // ring positions and parities
+        bool ok = true;
+        for (int t = first; ok && get_tile<BN, BR, 16>(a, off, tiles, t, w); t += stride) {
+            const uint32_t idesc = make_idesc(1, BF ? 1 : 0, BF ? 1 : 0, BM, (w.rows + 15) & ~15);
+            int in_group = 0;           // MMAs of the current group issued so far
+            for (int sb = dep.s0; ok && sb < dep.s1; ++sb) {
+                ok = wait_parity(smem_u32(&bar->x_full[xs]), xp, ctl, SITE_MMA) &&
+                     wait_parity(smem_u32(&bar->a_full[as]), ap, ctl, SITE_MMA);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+                const uint32_t a_tm = tmem + A_COL0 + as * A_COLS;
+                const uint64_t db = desc_x + xs * (X_BYTES >> 4);
+                const int steps = min(SK, a.K - sb * SK) / 16;
+                for (int k0 = 0; k0 < steps;) {
+                    if (in_group == 0) {
+                        ok = wait_parity(smem_u32(&bar->acc_empty[cs]), cp, ctl, SITE_MMA);
+                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                        tc_fence_after();
+                    }
+                    const int n = min(steps - k0, gsteps - in_group);
+                    if (leader) {
+                        for (int k = k0; k < k0 + n; k += 2) {  // steps, k0 and n are even
+                            const uint64_t d = db + (k >> 2) * (X_ATOM >> 4) + (k & 3) * 2;
+                            mma_f16_tmem_a(tmem + cs * BR, a_tm + k * 8, d, idesc, in_group + k - k0 > 0);
+                            mma_f16_tmem_a(tmem + cs * BR, a_tm + k * 8 + 8, d + 2, idesc, 1);
+                        }
+                        if (in_group + n == gsteps) tc_commit(smem_u32(&bar->acc_full[cs]));
+                    }
+                    __syncwarp();
+                    k0 += n;
+                    in_group += n;
+                    if (in_group == gsteps) {
+                        in_group = 0;
+                        if (++cs == ACCS) {
+                            cs = 0;
+                            cp ^= 1;
+                        }
+                    }
+                }
+                if (!ok) break;
+                if (leader) {
+                    tc_commit(smem_u32(&bar->a_empty[as]));
+                    tc_commit(smem_u32(&bar->x_empty[xs]));
+                }
+                __syncwarp();
+                if (++as == A_STAGES) {
+                    as = 0;
+                    ap ^= 1;
+                }
+                if (++xs == X_STAGES) {
+                    xs = 0;
+                    xp ^= 1;
+                }
+            }
+        }
+        if (leader) {
+            tc_commit(smem_u32(&bar->drain));
+            drain_parity(smem_u32(&bar->drain), 0, DRAIN_NS, a.status, SITE_DRAIN);
+        }
+        __syncwarp();
+    } else if (warp < SCALE_WARP0) {
+        // -------------------------------------------------------------------- rows of x
+        // Thread (16-byte chunk c of a stage's 256 bytes, row rr of every 4).  Padding repeats the last row; an
+        // index outside x reads row 0 (zeros are stored for it).
+        const int gt = (int)threadIdx.x - 64, c = gt & 15, rr = gt >> 4;
+        const size_t pitch = (size_t)a.K * 2;
+        uint32_t it = 0;
+        bool ok = true;
+        auto signal = [&](uint32_t i) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar->x_full[i % X_STAGES]));
+        };
+        for (int t = first; ok && get_tile<BN, BR, 16>(a, off, tiles, t, w); t += stride) {
+            const uint8_t *src[BR / 4];
+#pragma unroll
+            for (int j = 0; j < BR / 4; ++j) {
+                int v = w.r0 + min(4 * j + rr, w.rows - 1);
+                if (a.rows) v = __ldg(a.rows + v);
+                src[j] = a.x + ((unsigned)v < (unsigned)a.T ? (size_t)v : 0) * pitch;
+            }
+            const bool wide = w.rows > 16;
+            for (int sb = dep.s0; sb < dep.s1; ++sb, ++it) {
+                const uint32_t s = it % X_STAGES, u = it / X_STAGES;
+                ok = wait_parity(smem_u32(&bar->x_empty[s]), (u & 1) ^ 1, ctl, SITE_GATHER);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                const size_t at = (size_t)sb * (SK * 2) + c * 16;
+                const bool in = at < pitch;
+                const uint32_t dst = sX + s * X_BYTES + (c >> 3) * X_ATOM;
+#pragma unroll
+                for (int j = 0; j < BR / 4; ++j) {
+                    const int r = 4 * j + rr;
+                    if (j < 4 || wide) cp_async16(dst + r * 128 + (((c ^ r) & 7) << 4), src[j] + (in ? at : 0), in);
+                }
+                cp_async_commit();
+                if (it >= LAG) {
+                    cp_async_wait<LAG>();
+                    signal(it - LAG);
+                }
+            }
+        }
+        cp_async_wait<0>();
+        if (ok)
+            for (uint32_t i = it > LAG ? it - LAG : 0; i < it; ++i) signal(i);
+    } else if (warp < DQ_WARP0) {
+        // -------------------------------------------------------------------- scales, end of the tile
+        const int q = warp & 3, trow = 32 * q + lane;   // TMEM lanes 32 q ..; this lane's row of the tile
+        const uint32_t t_row = tmem + ((uint32_t)(32 * q) << 16);
+        const int g_first = (dep.s0 * SK) >> lg, g_last = min(groups, (dep.s1 * SK + a.gs - 1) >> lg);
+        const bool vec = groups % 8 == 0;
+        const uint16_t *srow = nullptr;
+        uint4 ns = {}, sc = {};     // scales of 8 groups: the next window's and the current one's
+        auto rows_of = [&](const Tile &t) {
+            const size_t wr = min((size_t)weight_row(t, trow >> 4) + (trow & 15), (size_t)a.E * a.N - 1);
+            srow = a.scales + wr * groups;
+        };
+        auto load = [&](int b) {
+            if (vec) {
+                ns = __ldg(reinterpret_cast<const uint4 *>(srow) + b);
+            } else {
+                uint32_t v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = __ldg(srow + min(8 * b + i, groups - 1));
+                ns = make_uint4(v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16));
+            }
+        };
+        uint32_t cs = 0, cp = 0, n = 0;
+        bool have = get_tile<BN, BR, 16>(a, off, tiles, first, w), ok = true;
+        if (have) {
+            rows_of(w);
+            load(g_first >> 3);
+        }
+        for (int t = first; ok && have; t += stride, ++n) {
+            const Tile cur = w;
+            const bool wide = cur.rows > 16;
+            // Rows of the tile whose index lies outside x.
+            bool out = false;
+            if (a.rows && lane < cur.rows) out = (unsigned)__ldg(a.rows + cur.r0 + lane) >= (unsigned)a.T;
+            const uint32_t zero_rows = __ballot_sync(0xffffffffu, out);
+            float acc[BR];
+#pragma unroll
+            for (int i = 0; i < BR; ++i) acc[i] = 0.0f;
+            // Scales come in windows of 8 groups, requested one window ahead, the next tile's first at the end.
+            int win = g_first >> 3;
+            sc = ns;
+            bool ahead = false;
+            auto request = [&](int b) {
+                if (8 * b < g_last) {
+                    load(b);
+                } else {
+                    have = get_tile<BN, BR, 16>(a, off, tiles, t + stride, w);
+                    if (have) {
+                        rows_of(w);
+                        load(g_first >> 3);
+                    }
+                    ahead = true;
+                }
+            };
+            request(win + 1);
+            for (int g = g_first; g < g_last; ++g) {
+                if ((g >> 3) != win) {
+                    win = g >> 3;
+                    sc = ns;
+                    request(win + 1);
+                }
+                const int i = g & 7;
+                const uint32_t pr = i < 4 ? (i < 2 ? sc.x : sc.y) : (i < 6 ? sc.z : sc.w);
+                const float s = half_bits_to_float((uint16_t)((i & 1) ? pr >> 16 : pr & 0xFFFFu));
+                ok = wait_parity(smem_u32(&bar->acc_full[cs]), cp, ctl, SITE_SCALE);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(t_row + cs * BR, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[j] = fmaf(s, __uint_as_float(r[j]), acc[j]);
+                if (wide) {
+                    tmem_ld_32x32b_x16(t_row + cs * BR + 16, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[16 + j] = fmaf(s, __uint_as_float(r[j]), acc[16 + j]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar->acc_empty[cs]));
+                if (++cs == ACCS) {
+                    cs = 0;
+                    cp ^= 1;
+                }
+            }
+            if (!ok) break;
+            if (!ahead) request(INT_MAX / 8);
+            if (split > 1) {
+                // Parts are added in rank order.  A lane's values lie 512 bytes apart, so that a warp's stores
+                // and loads are contiguous.
+                if (rank != 0) {
+                    if (n > 0) {
+                        ok = wait_parity(smem_u32(&bar->red_free[q]), (n - 1) & 1, ctl, SITE_SPLIT);
+                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    }
+                    const uint32_t dst = mapa_shared(sR + (rank - 1) * RED_BYTES + trow * 4, 0);
+#pragma unroll
+                    for (int j = 0; j < BR; ++j)
+                        if (j < 16 || wide) st_cluster_f32(dst + j * BM * 4, acc[j]);
+                    fence_cluster();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bar->red_full[q]), 0));
+                    continue;
+                }
+                ok = wait_parity(smem_u32(&bar->red_full[q]), n & 1, ctl, SITE_SPLIT);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                fence_cluster();
+                for (int c = 0; c < split - 1; ++c) {
+                    const float *part = reinterpret_cast<const float *>(base + OFF_RED + c * RED_BYTES) + trow;
+#pragma unroll
+                    for (int j = 0; j < BR; ++j)
+                        if (j < 16 || wide) acc[j] += part[j * BM];
+                }
+                __syncwarp();
+                if (lane > 0 && lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(&bar->red_free[q]), lane));
+            }
+            const int col = cur.n0 + (SWIGLU ? 16 * q + (lane & 15) : 32 * q + lane);
+            const bool col_ok = col < a.ldy;
+            uint16_t *yt = a.y + (size_t)cur.r0 * a.ldy + col;
+            if (SWIGLU) {
+                const bool up = lane >= 16;   // this lane's weight row is an up row
+#pragma unroll
+                for (int j = 0; j < BR; j += 2) {
+                    if (j >= 16 && !wide) break;
+                    const float other = __shfl_xor_sync(0xffffffffu, up ? acc[j] : acc[j + 1], 16);
+                    const float g = up ? other : acc[j], l = up ? acc[j + 1] : other;
+                    const int row = j + (up ? 1 : 0);
+                    if (row < cur.rows && col_ok)
+                        yt[(size_t)row * a.ldy] = (zero_rows >> row) & 1 ? (uint16_t)0 : round_bits<BF>(swiglu(g, l));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < BR; ++j)
+                    if (j < cur.rows && col_ok)
+                        yt[(size_t)j * a.ldy] = (zero_rows >> j) & 1 ? (uint16_t)0 : round_bits<BF>(acc[j]);
+            }
+        }
+    } else {
+        // -------------------------------------------------------------------- codes -> q - z
+        // Group d takes the stages d, d + 4, ... of a tile; a thread takes one weight row of them, 128 codes.
+        const int trow = 32 * (warp & 3) + lane, d = (warp - DQ_WARP0) >> 2;
+        const uint32_t t_a = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + A_COL0;
+        const uint32_t *zrow = nullptr;
+        const int nst = dep.s1 - dep.s0, packs = (nst + 1) / 2;
+        // Zeros come in words of 8 groups; a stage's groups lie in one word, requested a stage of this thread ahead.
+        uint32_t nz = 0;
+        int nw = 0;
+        auto word_of = [&](int j) { return min(((dep.s0 + j) * SK) >> lg, groups - 1) >> 3; };
+        auto rows_of = [&](const Tile &t) {
+            const size_t wr = min((size_t)weight_row(t, trow >> 4) + (trow & 15), (size_t)a.E * a.N - 1);
+            zrow = a.qzeros + wr * zwords;
+            nw = word_of(d);
+            nz = __ldg(zrow + nw);
+        };
+        uint32_t it0 = 0, pk0 = 0;          // ring positions of the tile's first stage and packed tile
+        bool ok = true, have = get_tile<BN, BR, 16>(a, off, tiles, first, w);
+        if (have) rows_of(w);
+        for (int t = first; ok && have; t += stride, it0 += nst, pk0 += packs) {
+            bool ahead = false;
+            auto next_tile = [&] {
+                have = get_tile<BN, BR, 16>(a, off, tiles, t + stride, w);
+                if (have) rows_of(w);
+                ahead = true;
+            };
+            for (int j = d; j < 2 * packs; j += 4) {
+                const uint32_t pk = pk0 + (j >> 1), p = pk % P_SLOTS;
+                ok = wait_parity(smem_u32(&bar->pk_full[p]), (pk / P_SLOTS) & 1, ctl, SITE_DEQUANT);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                if (j >= nst) {   // the depth ends inside the packed tile
+                    if (lane == 0) mbar_arrive(smem_u32(&bar->pk_empty[p]));
+                    continue;
+                }
+                // 128-byte swizzle: chunk c of row r lies at c ^ (r mod 8).
+                const uint32_t pr = sP + p * P_BYTES + trow * 128;
+                uint4 v[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] = lds128(pr + (((4 * (j & 1) + c) ^ (trow & 7)) << 4));
+                const uint32_t it = it0 + j, as = it % A_STAGES;
+                ok = wait_parity(smem_u32(&bar->a_empty[as]), ((it / A_STAGES) & 1) ^ 1, ctl, SITE_DEQUANT);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+                const int k0 = (dep.s0 + j) * SK;
+                const uint32_t cz = nz;
+                if (j + 4 < nst) {
+                    if (word_of(j + 4) != nw) {
+                        nw = word_of(j + 4);
+                        nz = __ldg(zrow + nw);
+                    }
+                } else {
+                    next_tile();
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {   // 32 codes, all in one group
+                    const int g = min((k0 + 32 * c) >> lg, groups - 1);
+                    const uint32_t z = (cz >> (4 * (g & 7))) & 0xFu;
+                    const uint32_t zc = BF ? 0xC300C300u + z * 0x00010001u : 0xD400E400u + z * 0x00100001u;
+                    uint32_t o[16];
+                    code_word<BF>(v[c].x, zc, o);
+                    code_word<BF>(v[c].y, zc, o + 4);
+                    code_word<BF>(v[c].z, zc, o + 8);
+                    code_word<BF>(v[c].w, zc, o + 12);
+                    tmem_st_32x32b_x16(t_a + as * A_COLS + c * 16, o);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&bar->pk_empty[p]));
+                    mbar_arrive(smem_u32(&bar->a_full[as]));
+                }
+            }
+            if (ok && !ahead) next_tile();
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (split > 1) cluster_sync();  // nothing of another CTA's still arrives here
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// CTAs of a cluster that share a tile's depth: the number (1, 2 or 4) with the shortest schedule, where a
+// round of tiles lasts its depth and a fixed part for the parts' exchange.
+int choose_split(long long tiles, int K, int sms) {
+    const int packs = ((K + SK - 1) / SK + 1) / 2;
+    int best = 1;
+    double best_t = 1e300;
+    for (int s = 1; s <= MAX_SPLIT; s *= 2) {
+        if (s > 1 && packs < 2 * s) break;
+        const long long clusters = sms / s, rounds = (tiles + clusters - 1) / clusters;
+        const double t = (double)rounds * ((double)packs / s + (s > 1 ? 1.0 : 0.0));
+        if (t < 0.98 * best_t) {
+            best_t = t;
+            best = s;
+        }
+    }
+    return best;
+}
+
+template <bool BF, bool SWIGLU>
+wq_status launch(const CUtensorMap &tw, const Args &a, long long tiles, cudaStream_t st, const char *who) {
+    auto kern = few_rows_kernel<BF, SWIGLU>;
+    const int split = choose_split(tiles, a.K, num_sms());
+    const size_t smem = smem_bytes(split, a.E);
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(MAX_SPLIT, MAX_E));
+    if (e != cudaSuccess) return fail(WQ_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", who, cudaGetErrorString(e));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<long long>(num_sms() / split, tiles) * split);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, tw, a, split);
+    if (e != cudaSuccess) return fail(WQ_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+    return WQ_OK;
+}
+
+}  // namespace
+
+wq_status few_rows_w4(const void *w, Args a, bool bf16, bool swiglu, cudaStream_t st, const char *who) {
+    a.ldy = swiglu ? a.N / 2 : a.N;
+    const int bn = swiglu ? BM / 2 : BM;
+    a.nb = (a.ldy + bn - 1) / bn;
+    const long long most = ((long long)std::min(a.E, a.R) + a.R / BR) * a.nb;  // tiles of any offsets
+    WQ_REQUIRE(most < INT_MAX / 2, WQ_ERR_UNSUPPORTED, "%s: R (%d) x N (%d) gives too many tiles", who, a.R, a.N);
+    CUtensorMap tw;
+    if (!encode_weights(&tw, w, (uint64_t)a.K / 2, a, swiglu)) return WQ_ERR_CUDA;
+    if (bf16) return swiglu ? launch<true, true>(tw, a, most, st, who) : launch<true, false>(tw, a, most, st, who);
+    return swiglu ? launch<false, true>(tw, a, most, st, who) : launch<false, false>(tw, a, most, st, who);
+}
+
+}  // namespace grouped
+}  // namespace wq

@@ -30,9 +30,7 @@
 //   then        four warps that gather indexed activation rows by cp.async (TMA's gather of four rows a
 //               request took 32 cycles for its 512 bytes, four times what the MMAs leave), and for INT4
 //               four groups of four warps that dequantize every fourth stage each
-#include "sm100.cuh"
-#include "wq_device.cuh"
-#include "wq_host.h"
+#include "grouped.cuh"
 
 #include <algorithm>
 #include <climits>
@@ -41,19 +39,17 @@ namespace wq {
 namespace {
 
 using namespace sm100;
+using namespace grouped;
 
 enum Kind { K_I8, K_FP8, K_W4H, K_W4B };  // INT8, E4M3, INT4 weights with fp16 / bf16 activations
 
-constexpr int BM = 128;                // weight rows of a CTA's share of a tile
 constexpr int STAGE_K = 128;           // bytes of k per stage and row (128 INT8/FP8 or 64 16-bit values)
 constexpr uint32_t A_BYTES = BM * STAGE_K;
 constexpr int PK = 4;                  // stages per packed INT4 tile (128 bytes of a weight row)
 constexpr uint32_t P_BYTES = BM * PK * 32;
-constexpr int MAX_E = 512;
 constexpr int EPI_WARP0 = 4, GATHER_WARPS = 4, DQ_GROUPS = 4;
 constexpr int LAG = 2;                 // stages of gathered rows in flight per thread
-constexpr int MAX_STAGES = 8, MAX_PSTAGES = 4;
-constexpr uint64_t DRAIN_NS = 2000000000ull;
+constexpr int MAX_STAGES = 8, MAX_PSTAGES = 3;
 constexpr unsigned SITE_PRODUCER = 0x1001, SITE_MMA = 0x1002, SITE_EPILOGUE = 0x1004, SITE_DRAIN = 0x1008,
                    SITE_DEQUANT = 0x1010, SITE_PACKED = 0x1020, SITE_GATHER = 0x1040;
 
@@ -76,8 +72,8 @@ struct Layout {
     static constexpr int BR = PAIR ? 256 : 64;               // activation rows of a tile, at most
     static constexpr int SR = PAIR ? BR / 2 : BR;            // of them in this CTA's shared memory
     static constexpr uint32_t B_BYTES = SR * STAGE_K;
-    static constexpr int STAGES = PAIR ? (W4 ? 5 : 6) : (W4 ? 6 : 8);
-    static constexpr int PSTAGES = PAIR ? 3 : 4;             // packed INT4 tiles
+    static constexpr int STAGES = PAIR ? (W4 ? 5 : 6) : 8;
+    static constexpr int PSTAGES = 3;                        // packed INT4 tiles
     static constexpr int BOX = PAIR ? 64 : 16;               // rows per box when the activations lie in order
     static constexpr int GA_WARP0 = 8;
     static constexpr int DQ_WARP0 = GA_WARP0 + (GATHER ? GATHER_WARPS : 0);
@@ -89,81 +85,11 @@ struct Layout {
     static constexpr uint32_t OFF_SX = OFF_SRC + 2 * BR * 4;              // float [2][BR] (8-bit kinds)
     static constexpr uint32_t OFF_TAB = OFF_SX + (W4 ? 0 : 2 * BR * 4);   // int offsets[E + 1], tiles[E + 1]
     static constexpr size_t smem(int E) { return 1024 + OFF_TAB + 2 * (size_t)(E + 1) * 4; }
+    static_assert(PAIR || !W4, "INT4 with few rows has a kernel of its own");
     static_assert(smem(MAX_E) <= 232448, "fits the shared memory of a CTA");
     static_assert(STAGES <= MAX_STAGES && PSTAGES <= MAX_PSTAGES && STAGES > LAG, "barrier arrays, gather lag");
 };
 static_assert(sizeof(Bars) <= 1024, "barriers fit their space");
-
-struct Args {
-    const uint8_t *x;                // [T] rows
-    const int32_t *offsets, *rows;   // rows null: row p of x itself
-    const float *sx, *sw;
-    int sx_stride, sw_per_row;
-    const uint16_t *scales;          // INT4: fp16 [E][N][K/gs]
-    const uint32_t *qzeros;
-    uint16_t *y;
-    int T, R, E, N, K, gs;           // T: rows of x, R: grouped rows
-    int nb;                          // weight-row blocks per expert
-    int box;                         // SwiGLU: the weight map is the 5-D one (see load_weights)
-    int ldy;                         // columns of y (N, or N / 2 with SwiGLU)
-    unsigned int *status;
-    uint64_t limit_ns;
-};
-
-struct Tile {
-    int e, n0;        // expert, first output column of the tile
-    int r0, rows;     // first grouped row, number of rows
-};
-
-// Offsets clamped to [0, R] and made non-decreasing (a valid array is unchanged), and the exclusive
-// prefix of the experts' tile counts; by one warp.
-template <int BR>
-__device__ __forceinline__ void build_table(const Args &a, int *off, int *tiles, int lane) {
-    int high = 0;
-    for (int i0 = 0; i0 <= a.E; i0 += 32) {
-        int v = i0 + lane <= a.E ? min(max(__ldg(a.offsets + i0 + lane), 0), a.R) : 0;
-        v = max(v, high);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) v = max(v, __shfl_up_sync(0xffffffffu, v, o));
-        if (i0 + lane <= a.E) off[i0 + lane] = v;
-        high = __shfl_sync(0xffffffffu, v, 31);
-    }
-    __syncwarp();
-    int run = 0;
-    for (int i0 = 0; i0 < a.E; i0 += 32) {
-        const int v = i0 + lane < a.E ? (off[i0 + lane + 1] - off[i0 + lane] + BR - 1) / BR * a.nb : 0;
-        int s = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int n = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += n;
-        }
-        if (i0 + lane < a.E) tiles[i0 + lane] = run + s - v;
-        run += __shfl_sync(0xffffffffu, s, 31);
-    }
-    if (lane == 0) tiles[a.E] = run;
-}
-
-// Tile t of the list; false past its end.  BN: output columns per tile, BR and STEP: most rows of a block
-// and what its length is rounded up to.
-template <int BN, int BR, int STEP>
-__device__ __forceinline__ bool get_tile(const Args &a, const int *off, const int *tiles, int t, Tile &w) {
-    if (t >= tiles[a.E]) return false;
-    int lo = 0, hi = a.E;  // the expert e with tiles[e] <= t < tiles[e + 1]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (tiles[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    const int first = off[lo], n = off[lo + 1] - first, rb = (n + BR - 1) / BR;
-    const int per = ((n + rb - 1) / rb + STEP - 1) / STEP * STEP;
-    const int local = t - tiles[lo], b = local % rb;
-    w.e = lo;
-    w.n0 = (local / rb) * BN;
-    w.r0 = first + b * per;
-    w.rows = min(per, n - b * per);
-    return true;
-}
 
 template <Kind KIND, bool PAIR>
 __device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -182,24 +108,6 @@ template <Kind KIND>
 __host__ __device__ constexpr uint32_t idesc_rows(int m, int rows) {
     return KIND == K_I8 ? make_idesc(2, 1, 1, m, rows)
                         : make_idesc(1, KIND == K_W4B ? 1 : 0, KIND == K_W4B ? 1 : 0, m, rows);
-}
-
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-    uint32_t d;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-    return d;
-}
-
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t d;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
 }
 
 __device__ __forceinline__ uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
@@ -253,20 +161,6 @@ __device__ __forceinline__ uint4 dequant_word(uint32_t w, const GroupConst<BF> &
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
-
-__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-
-// silu(g) u.  The fast exponential and division are off by a few fp32 units, far below the 16-bit
-// rounding that follows.
-__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 template <Kind KIND>
 __device__ __forceinline__ uint16_t out_bits(float v) {
@@ -724,9 +618,6 @@ bool choose_pair(const Args &a) { return (long long)a.R >= 48ll * std::min(a.E, 
 template <Kind KIND, bool PAIR>
 wq_status dispatch(const void *w, Args a, bool swiglu, cudaStream_t st, const char *who) {
     constexpr bool W4 = is_w4(KIND);
-    a.status = device_status_word();
-    if (!a.status) return WQ_ERR_CUDA;
-    a.limit_ns = wait_limit();
     a.ldy = swiglu ? a.N / 2 : a.N;
     const int bn = (swiglu ? BM / 2 : BM) * (PAIR ? 2 : 1), br = Layout<KIND, false, PAIR>::BR;
     a.nb = (a.ldy + bn - 1) / bn;
@@ -741,18 +632,7 @@ wq_status dispatch(const void *w, Args a, bool swiglu, cudaStream_t st, const ch
                         Layout<KIND, false, PAIR>::BOX,
                         CU_TENSOR_MAP_SWIZZLE_128B))
         return WQ_ERR_CUDA;
-    const uint64_t wbytes = W4 ? (uint64_t)a.K / 2 : (uint64_t)a.K, half = (uint64_t)a.N / 2;
-    a.box = swiglu && half % 16 == 0;
-    if (a.box) {
-        const uint64_t dims[5] = {wbytes, 16, 2, half / 16, (uint64_t)a.E};
-        const uint64_t strides[4] = {wbytes, half * wbytes, 16 * wbytes, (uint64_t)a.N * wbytes};
-        const uint32_t box[5] = {STAGE_K, 16, 2, 4, 1};
-        if (!encode_tmap(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, w, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
-            return WQ_ERR_CUDA;
-    } else if (!encode_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, wbytes, (uint64_t)a.E * a.N, wbytes, STAGE_K,
-                               swiglu ? 16 : BM, CU_TENSOR_MAP_SWIZZLE_128B)) {
-        return WQ_ERR_CUDA;
-    }
+    if (!encode_weights(&tw, w, W4 ? (uint64_t)a.K / 2 : (uint64_t)a.K, a, swiglu)) return WQ_ERR_CUDA;
     if (gather)
         return swiglu ? launch<KIND, true, true, PAIR>(tx, tw, a, most, st, who)
                       : launch<KIND, true, false, PAIR>(tx, tw, a, most, st, who);
@@ -763,8 +643,29 @@ wq_status dispatch(const void *w, Args a, bool swiglu, cudaStream_t st, const ch
 template <Kind KIND>
 wq_status run(const void *x, const void *w, Args a, bool swiglu, cudaStream_t st, const char *who) {
     a.x = static_cast<const uint8_t *>(x);
-    return choose_pair(a) ? dispatch<KIND, true>(w, a, swiglu, st, who) : dispatch<KIND, false>(w, a, swiglu, st, who);
+    a.status = device_status_word();
+    if (!a.status) return WQ_ERR_CUDA;
+    a.limit_ns = wait_limit();
+    if (choose_pair(a)) return dispatch<KIND, true>(w, a, swiglu, st, who);
+    if constexpr (is_w4(KIND)) return few_rows_w4(w, a, KIND == K_W4B, swiglu, st, who);
+    else return dispatch<KIND, false>(w, a, swiglu, st, who);
 }
+
+}  // namespace
+
+bool grouped::encode_weights(CUtensorMap *map, const void *w, uint64_t row_bytes, Args &a, bool swiglu) {
+    const uint64_t half = (uint64_t)a.N / 2;
+    a.box = swiglu && half % 16 == 0;
+    if (!a.box)
+        return encode_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, row_bytes, (uint64_t)a.E * a.N, row_bytes, 128,
+                              swiglu ? 16 : BM, CU_TENSOR_MAP_SWIZZLE_128B);
+    const uint64_t dims[5] = {row_bytes, 16, 2, half / 16, (uint64_t)a.E};
+    const uint64_t strides[4] = {row_bytes, half * row_bytes, 16 * row_bytes, (uint64_t)a.N * row_bytes};
+    const uint32_t box[5] = {128, 16, 2, 4, 1};
+    return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, w, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+namespace {
 
 // Checks that every grouped product makes of its sizes.
 wq_status check_sizes(const char *who, int T, const int32_t *rows, const int32_t *offsets, int R, int E, int N, int K,
