@@ -3,21 +3,24 @@
 //
 //   y[p][n] = sum_j s[n][j] * ( sum_{k in group j} (q[n][k] - z[n][j]) x[rows[p]][k] )
 //
-// With 16 or 32 activation rows a weight takes part in so few products that turning it into an fp16 value
+// With up to 16 activation rows a weight takes part in so few products that turning it into an fp16 value
 // s (q - z) would cost more than the tensor cores' work on it.  So the MMA's operand is q - z itself, an
 // integer of 5 bits that fp16 and bf16 hold exactly, every group of codes has an accumulator of its own in
-// tensor memory, and the group's scale multiplies the 128 x rows sums in fp32 when the group is done: no
+// tensor memory, and the group's scale multiplies the 128 x 16 sums in fp32 when the group is done: no
 // weight is rounded, and a scale costs one fma per row of x instead of one product per code.
 //
-// Persistent CTA, one per SM; a tile is 128 weight rows times up to 32 rows of one expert, and the S CTAs
+// Persistent CTA, one per SM; a tile is 128 weight rows times up to 16 rows of one expert, and the S CTAs
 // of a cluster share a tile's depth, so that the last round of tiles is short:
-//   warp 0       TMA: 128 rows x 128 bytes (256 codes) of packed weights into a deep ring
-//   warp 1       an elected thread issues tcgen05.mma (A from tensor memory, 128 codes per stage)
-//   warps 2, 3   (2 allocates tensor memory) rows of x by cp.async, 128-byte swizzle
-//   warps 4-7    scale: each group's accumulator, times the scale of the lane's weight row, into registers;
+//   warp 0       TMA: 128 rows x 128 bytes (a pack of 256 codes) of packed weights into a deep ring
+//   warps 1, 2   an elected thread each issues tcgen05.mma for every other pack (A from tensor memory): a
+//                wait takes a thread about 100 cycles even when it is over, an MMA 45 and a commit 50, so
+//                one thread alone cannot issue 16 MMAs of 16 codes in the 710 cycles that a pack's bytes take
+//   warp 3       allocates tensor memory
+//   warps 4-7    scale: each pack's accumulators, times the scales of the lane's weight row, into registers;
 //                at the end of a tile the cluster's parts meet in the first CTA's shared memory, which
 //                applies SwiGLU, rounds and stores
-//   warps 8-23   four groups of four warps: codes -> q - z into tensor memory, every fourth stage each
+//   warps 8-23   four groups of four warps, every fourth stage (half a pack) each: rows of x by cp.async, and
+//                codes -> q - z into tensor memory
 #include "grouped.cuh"
 
 #include <algorithm>
@@ -29,29 +32,32 @@ namespace {
 
 using namespace sm100;
 
-constexpr int BR = 32;                      // rows of a tile, at most (16 or 32)
+constexpr int BR = 16;                      // rows of a tile, at most (the MMA's N)
 constexpr int SK = 128;                     // codes per stage
-constexpr int A_STAGES = 4, X_STAGES = 6, P_SLOTS = 7, ACCS = 8, LAG = 3;
+constexpr int STAGES = 4, P_SLOTS = 8, MAX_ACCS = 8;
 constexpr uint32_t X_ATOM = BR * 128, X_BYTES = 2 * X_ATOM;   // 64 values a row and atom
-constexpr uint32_t P_BYTES = BM * 128;      // 256 codes of 128 rows: two stages
+constexpr uint32_t P_BYTES = BM * 128;      // a pack: 256 codes of 128 rows, two stages
 constexpr uint32_t A_COLS = SK / 2;         // tensor memory columns of a stage
-constexpr uint32_t A_COL0 = ACCS * BR;      // after the accumulators
 constexpr int THREADS = 768, SCALE_WARP0 = 4, DQ_WARP0 = 8;
 constexpr int MAX_SPLIT = 4;
 constexpr uint32_t OFF_X = P_SLOTS * P_BYTES;
-constexpr uint32_t OFF_RED = OFF_X + X_STAGES * X_BYTES;      // not used when the tile is not split
+constexpr uint32_t OFF_RED = OFF_X + STAGES * X_BYTES;    // not used when the tile is not split
 constexpr uint32_t RED_BYTES = BM * BR * 4;                   // one CTA's part of a tile
-constexpr unsigned SITE_PACKED = 0x2001, SITE_MMA = 0x2002, SITE_GATHER = 0x2004, SITE_SCALE = 0x2008,
-                   SITE_DEQUANT = 0x2010, SITE_DRAIN = 0x2020, SITE_SPLIT = 0x2040;
-static_assert(A_COL0 + A_STAGES * A_COLS <= 512, "tensor memory");
+constexpr unsigned SITE_PACKED = 0x2001, SITE_MMA = 0x2002, SITE_SCALE = 0x2008, SITE_DEQUANT = 0x2010,
+                   SITE_DRAIN = 0x2020, SITE_SPLIT = 0x2040;
+
+// Tensor memory: four stages of 64 columns, then accumulators, 16 columns per group and 256 / gs groups per pack.
+// Stage and accumulator slots belong to one dequantizing group and one issuer each (4 stages, an even number
+// of accumulators): a thread that waited for a slot another one had not used yet could take an older phase of
+// its barrier, of the same parity, for the one it waits for.
+static_assert(STAGES * A_COLS + 256 * BR / 16 <= 512, "tensor memory");
 
 struct Bars {
     uint64_t pk_full[P_SLOTS], pk_empty[P_SLOTS];
-    uint64_t x_full[X_STAGES], x_empty[X_STAGES];
-    uint64_t a_full[A_STAGES], a_empty[A_STAGES];
-    uint64_t acc_full[ACCS], acc_empty[ACCS];
+    uint64_t full[STAGES], empty[STAGES];       // rows of x and q - z of a stage
+    uint64_t acc_full[MAX_ACCS], acc_empty[MAX_ACCS];   // accumulators of a pack
     uint64_t red_full[4], red_free[4];      // per scale warp: the other CTAs' parts are here / may be sent
-    uint64_t drain;
+    uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
 };
@@ -60,7 +66,7 @@ constexpr size_t smem_bytes(int split, int E) {
     return 1024 + OFF_RED + (size_t)(split - 1) * RED_BYTES + 1024 + 2 * (size_t)(E + 1) * 4;
 }
 
-static_assert(smem_bytes(MAX_SPLIT, MAX_E) <= 232448 && sizeof(Bars) <= 1024 && X_STAGES > LAG, "shared memory");
+static_assert(smem_bytes(MAX_SPLIT, MAX_E) <= 232448 && sizeof(Bars) <= 1024, "shared memory");
 
 // q - z of the 8 codes of a word, in k order, as fp16 or bf16 pairs.  zc: the fp16 pair -(1024 + z),
 // -(64 + z), or the bf16 pair -(128 + z) twice (see dequant_word in grouped_gemm.cu).
@@ -108,6 +114,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int rank = split > 1 ? (int)cluster_ctarank() : 0;
     const int first = (int)blockIdx.x / split, stride = (int)gridDim.x / split;
     const Depth dep(a.K, rank, split);
+    const int nst = dep.s1 - dep.s0, packs = (nst + 1) / 2;   // of a tile, in this CTA
+    const int accs = min(a.gs / 16, MAX_ACCS), acc_cols = 256 / a.gs * BR;
     const int lg = 31 - __clz(a.gs), groups = a.K >> lg, zwords = (groups + 7) / 8;
 
     if (threadIdx.x == 0) {
@@ -115,15 +123,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(smem_u32(&bar->pk_full[i]), 1);
             mbar_init(smem_u32(&bar->pk_empty[i]), 8);
         }
-        for (int i = 0; i < X_STAGES; ++i) {
-            mbar_init(smem_u32(&bar->x_full[i]), 2);
-            mbar_init(smem_u32(&bar->x_empty[i]), 1);
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(smem_u32(&bar->full[i]), 4);
+            mbar_init(smem_u32(&bar->empty[i]), 1);
         }
-        for (int i = 0; i < A_STAGES; ++i) {
-            mbar_init(smem_u32(&bar->a_full[i]), 4);
-            mbar_init(smem_u32(&bar->a_empty[i]), 1);
-        }
-        for (int i = 0; i < ACCS; ++i) {
+        for (int i = 0; i < MAX_ACCS; ++i) {
             mbar_init(smem_u32(&bar->acc_full[i]), 1);
             mbar_init(smem_u32(&bar->acc_empty[i]), 4);
         }
@@ -131,13 +135,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(smem_u32(&bar->red_full[i]), max(1, split - 1));
             mbar_init(smem_u32(&bar->red_free[i]), 1);
         }
-        mbar_init(smem_u32(&bar->drain), 1);
+        mbar_init(smem_u32(&bar->drain[0]), 1);
+        mbar_init(smem_u32(&bar->drain[1]), 1);
         bar->abort = 0;
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) prefetch_tmap(&tmap_w);
     if (warp == 1) build_table<BR>(a, off, tiles, lane);
-    if (warp == 2) {
+    if (warp == 3) {
         tmem_alloc(smem_u32(&bar->tmem_base), 512);
         tmem_relinquish();
     }
@@ -159,7 +164,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool leader = elect_one();
         uint32_t p = 0, ph = 1, it = 0;
         bool ok = true;
-        for (int t = first; ok && get_tile<BN, BR, 16>(a, off, tiles, t, w); t += stride) {
+        for (int t = first; ok && get_tile<BN, BR, BR>(a, off, tiles, t, w); t += stride) {
             for (int sb = dep.s0; sb < dep.s1; sb += 2, ++it) {
                 ok = wait_parity(smem_u32(&bar->pk_empty[p]), ph, ctl, SITE_PACKED);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -187,115 +192,52 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (issued) drain_parity(smem_u32(&bar->pk_full[i]), (issued - 1) & 1, DRAIN_NS, a.status, SITE_DRAIN);
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // -------------------------------------------------------------------- MMA issuer
+    } else if (warp <= 2) {
+        // -------------------------------------------------------------------- MMA issuers
         const bool leader = elect_one();
+        const int me = warp - 1;
         const uint64_t desc_x = umma_desc_sw128_kmajor(sX);
-        const int gsteps = a.gs / 16;   // MMAs (16 codes) per group
-        uint32_t as = 0, ap = 0, xs = 0, xp = 0, cs = 0, cp = 1;  // ring positions and parities
+        constexpr uint32_t IDESC = make_idesc(1, BF ? 1 : 0, BF ? 1 : 0, BM, BR);
+        const int gmask = a.gs / 16 - 1;             // MMAs (16 codes) per group, less one
+        uint32_t pk = 0;                             // packs before this tile
         bool ok = true;
-        for (int t = first; ok && get_tile<BN, BR, 16>(a, off, tiles, t, w); t += stride) {
-            const uint32_t idesc = make_idesc(1, BF ? 1 : 0, BF ? 1 : 0, BM, (w.rows + 15) & ~15);
-            int in_group = 0;           // MMAs of the current group issued so far
-            for (int sb = dep.s0; ok && sb < dep.s1; ++sb) {
-                ok = wait_parity(smem_u32(&bar->x_full[xs]), xp, ctl, SITE_MMA) &&
-                     wait_parity(smem_u32(&bar->a_full[as]), ap, ctl, SITE_MMA);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                tc_fence_after();
-                const uint32_t a_tm = tmem + A_COL0 + as * A_COLS;
-                const uint64_t db = desc_x + xs * (X_BYTES >> 4);
-                const int steps = min(SK, a.K - sb * SK) / 16;
-                for (int k0 = 0; k0 < steps;) {
-                    if (in_group == 0) {
-                        ok = wait_parity(smem_u32(&bar->acc_empty[cs]), cp, ctl, SITE_MMA);
-                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                        tc_fence_after();
-                    }
-                    const int n = min(steps - k0, gsteps - in_group);
+        for (int t = first; ok && get_tile<BN, BR, BR>(a, off, tiles, t, w); t += stride, pk += packs) {
+            for (int b = (int)((me - pk) & 1); b < packs; b += 2) {
+                const uint32_t c = (pk + b) % accs, cu = (pk + b) / accs;
+                const uint32_t acc = tmem + STAGES * A_COLS + c * acc_cols;
+                const uint32_t ae = smem_u32(&bar->acc_empty[c]);
+                for (int h = 0; h < 2; ++h) {   // the second stage of the last pack may be empty
+                    const uint32_t it = 2 * (pk + b) + h, s = it % STAGES, u = it / STAGES;
+                    const uint32_t fb = smem_u32(&bar->full[s]);
+                    ok = h == 0 ? wait_parity2(ae, (cu & 1) ^ 1, fb, u & 1, ctl, SITE_MMA)
+                                : wait_parity(fb, u & 1, ctl, SITE_MMA);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    tc_fence_after();
                     if (leader) {
-                        for (int k = k0; k < k0 + n; k += 2) {  // steps, k0 and n are even
-                            const uint64_t d = db + (k >> 2) * (X_ATOM >> 4) + (k & 3) * 2;
-                            mma_f16_tmem_a(tmem + cs * BR, a_tm + k * 8, d, idesc, in_group + k - k0 > 0);
-                            mma_f16_tmem_a(tmem + cs * BR, a_tm + k * 8 + 8, d + 2, idesc, 1);
-                        }
-                        if (in_group + n == gsteps) tc_commit(smem_u32(&bar->acc_full[cs]));
+                        const uint32_t a_tm = tmem + s * A_COLS;
+                        const uint64_t db = desc_x + s * (X_BYTES >> 4);
+                        const int steps = (a.K - (dep.s0 + 2 * b + h) * SK) / 16;
+#pragma unroll
+                        for (int k = 0; k < SK / 16; ++k)
+                            if (k < steps)
+                                mma_f16_tmem_a(acc + (((8 * h + k) * 16) >> lg) * BR, a_tm + k * 8,
+                                               db + (k >> 2) * (X_ATOM >> 4) + (k & 3) * 2, IDESC,
+                                               ((8 * h + k) & gmask) != 0);
+                        tc_commit(smem_u32(&bar->empty[s]));
                     }
                     __syncwarp();
-                    k0 += n;
-                    in_group += n;
-                    if (in_group == gsteps) {
-                        in_group = 0;
-                        if (++cs == ACCS) {
-                            cs = 0;
-                            cp ^= 1;
-                        }
-                    }
                 }
                 if (!ok) break;
-                if (leader) {
-                    tc_commit(smem_u32(&bar->a_empty[as]));
-                    tc_commit(smem_u32(&bar->x_empty[xs]));
-                }
+                if (leader) tc_commit(smem_u32(&bar->acc_full[c]));
                 __syncwarp();
-                if (++as == A_STAGES) {
-                    as = 0;
-                    ap ^= 1;
-                }
-                if (++xs == X_STAGES) {
-                    xs = 0;
-                    xp ^= 1;
-                }
             }
         }
         if (leader) {
-            tc_commit(smem_u32(&bar->drain));
-            drain_parity(smem_u32(&bar->drain), 0, DRAIN_NS, a.status, SITE_DRAIN);
+            tc_commit(smem_u32(&bar->drain[me]));
+            drain_parity(smem_u32(&bar->drain[me]), 0, DRAIN_NS, a.status, SITE_DRAIN);
         }
         __syncwarp();
-    } else if (warp < SCALE_WARP0) {
-        // -------------------------------------------------------------------- rows of x
-        // Thread (16-byte chunk c of a stage's 256 bytes, row rr of every 4).  Padding repeats the last row; an
-        // index outside x reads row 0 (zeros are stored for it).
-        const int gt = (int)threadIdx.x - 64, c = gt & 15, rr = gt >> 4;
-        const size_t pitch = (size_t)a.K * 2;
-        uint32_t it = 0;
-        bool ok = true;
-        auto signal = [&](uint32_t i) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bar->x_full[i % X_STAGES]));
-        };
-        for (int t = first; ok && get_tile<BN, BR, 16>(a, off, tiles, t, w); t += stride) {
-            const uint8_t *src[BR / 4];
-#pragma unroll
-            for (int j = 0; j < BR / 4; ++j) {
-                int v = w.r0 + min(4 * j + rr, w.rows - 1);
-                if (a.rows) v = __ldg(a.rows + v);
-                src[j] = a.x + ((unsigned)v < (unsigned)a.T ? (size_t)v : 0) * pitch;
-            }
-            const bool wide = w.rows > 16;
-            for (int sb = dep.s0; sb < dep.s1; ++sb, ++it) {
-                const uint32_t s = it % X_STAGES, u = it / X_STAGES;
-                ok = wait_parity(smem_u32(&bar->x_empty[s]), (u & 1) ^ 1, ctl, SITE_GATHER);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                const size_t at = (size_t)sb * (SK * 2) + c * 16;
-                const bool in = at < pitch;
-                const uint32_t dst = sX + s * X_BYTES + (c >> 3) * X_ATOM;
-#pragma unroll
-                for (int j = 0; j < BR / 4; ++j) {
-                    const int r = 4 * j + rr;
-                    if (j < 4 || wide) cp_async16(dst + r * 128 + (((c ^ r) & 7) << 4), src[j] + (in ? at : 0), in);
-                }
-                cp_async_commit();
-                if (it >= LAG) {
-                    cp_async_wait<LAG>();
-                    signal(it - LAG);
-                }
-            }
-        }
-        cp_async_wait<0>();
-        if (ok)
-            for (uint32_t i = it > LAG ? it - LAG : 0; i < it; ++i) signal(i);
+    } else if (warp == 3) {
     } else if (warp < DQ_WARP0) {
         // -------------------------------------------------------------------- scales, end of the tile
         const int q = warp & 3, trow = 32 * q + lane;   // TMEM lanes 32 q ..; this lane's row of the tile
@@ -318,15 +260,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ns = make_uint4(v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16));
             }
         };
-        uint32_t cs = 0, cp = 0, n = 0;
-        bool have = get_tile<BN, BR, 16>(a, off, tiles, first, w), ok = true;
+        uint32_t pk = 0, n = 0;
+        bool have = get_tile<BN, BR, BR>(a, off, tiles, first, w), ok = true;
         if (have) {
             rows_of(w);
             load(g_first >> 3);
         }
         for (int t = first; ok && have; t += stride, ++n) {
             const Tile cur = w;
-            const bool wide = cur.rows > 16;
             // Rows of the tile whose index lies outside x.
             bool out = false;
             if (a.rows && lane < cur.rows) out = (unsigned)__ldg(a.rows + cur.r0 + lane) >= (unsigned)a.T;
@@ -342,7 +283,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (8 * b < g_last) {
                     load(b);
                 } else {
-                    have = get_tile<BN, BR, 16>(a, off, tiles, t + stride, w);
+                    have = get_tile<BN, BR, BR>(a, off, tiles, t + stride, w);
                     if (have) {
                         rows_of(w);
                         load(g_first >> 3);
@@ -351,7 +292,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             };
             request(win + 1);
-            for (int g = g_first; g < g_last; ++g) {
+            auto scale = [&](int g) {
                 if ((g >> 3) != win) {
                     win = g >> 3;
                     sc = ns;
@@ -359,28 +300,39 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 const int i = g & 7;
                 const uint32_t pr = i < 4 ? (i < 2 ? sc.x : sc.y) : (i < 6 ? sc.z : sc.w);
-                const float s = half_bits_to_float((uint16_t)((i & 1) ? pr >> 16 : pr & 0xFFFFu));
-                ok = wait_parity(smem_u32(&bar->acc_full[cs]), cp, ctl, SITE_SCALE);
+                return half_bits_to_float((uint16_t)((i & 1) ? pr >> 16 : pr & 0xFFFFu));
+            };
+            int g = g_first;
+            for (int b = 0; b < packs; ++b, ++pk) {
+                const uint32_t c = pk % accs, cols = t_row + STAGES * A_COLS + c * acc_cols;
+                ok = wait_parity(smem_u32(&bar->acc_full[c]), (pk / accs) & 1, ctl, SITE_SCALE);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
-                uint32_t r[16];
-                tmem_ld_32x32b_x16(t_row + cs * BR, r);
-                tmem_ld_wait();
+                const int end = min(g_last, g + max(1, 256 >> lg));
+                for (int i = 0; g < end; g += 2, i += 2) {   // two groups at a time
+                    uint32_t r[32];
+                    const bool two = g + 1 < end;
+                    if (two) {
+                        tmem_ld_32x32b_x32(cols + i * BR, r);
+                    } else {
+                        uint32_t r1[16];
+                        tmem_ld_32x32b_x16(cols + i * BR, r1);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) acc[j] = fmaf(s, __uint_as_float(r[j]), acc[j]);
-                if (wide) {
-                    tmem_ld_32x32b_x16(t_row + cs * BR + 16, r);
+                        for (int j = 0; j < 16; ++j) r[j] = r1[j];
+                    }
+                    const float s0 = scale(g), s1 = two ? scale(g + 1) : 0.0f;
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) acc[16 + j] = fmaf(s, __uint_as_float(r[j]), acc[16 + j]);
+                    for (int j = 0; j < BR; ++j) acc[j] = fmaf(s0, __uint_as_float(r[j]), acc[j]);
+                    if (two) {
+#pragma unroll
+                        for (int j = 0; j < BR; ++j) acc[j] = fmaf(s1, __uint_as_float(r[16 + j]), acc[j]);
+                    }
                 }
+                g = end;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar->acc_empty[cs]));
-                if (++cs == ACCS) {
-                    cs = 0;
-                    cp ^= 1;
-                }
+                if (lane == 0) mbar_arrive(smem_u32(&bar->acc_empty[c]));
             }
             if (!ok) break;
             if (!ahead) request(INT_MAX / 8);
@@ -395,7 +347,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const uint32_t dst = mapa_shared(sR + (rank - 1) * RED_BYTES + trow * 4, 0);
 #pragma unroll
                     for (int j = 0; j < BR; ++j)
-                        if (j < 16 || wide) st_cluster_f32(dst + j * BM * 4, acc[j]);
+                        st_cluster_f32(dst + j * BM * 4, acc[j]);
                     fence_cluster();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bar->red_full[q]), 0));
@@ -408,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const float *part = reinterpret_cast<const float *>(base + OFF_RED + c * RED_BYTES) + trow;
 #pragma unroll
                     for (int j = 0; j < BR; ++j)
-                        if (j < 16 || wide) acc[j] += part[j * BM];
+                        acc[j] += part[j * BM];
                 }
                 __syncwarp();
                 if (lane > 0 && lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(&bar->red_free[q]), lane));
@@ -420,7 +372,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const bool up = lane >= 16;   // this lane's weight row is an up row
 #pragma unroll
                 for (int j = 0; j < BR; j += 2) {
-                    if (j >= 16 && !wide) break;
                     const float other = __shfl_xor_sync(0xffffffffu, up ? acc[j] : acc[j + 1], 16);
                     const float g = up ? other : acc[j], l = up ? acc[j + 1] : other;
                     const int row = j + (up ? 1 : 0);
@@ -436,48 +387,74 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else {
         // -------------------------------------------------------------------- codes -> q - z
-        // Group d takes the stages d, d + 4, ... of a tile; a thread takes one weight row of them, 128 codes.
+        // Group d takes every fourth stage; a thread takes one weight row of it, 128 codes.
         const int trow = 32 * (warp & 3) + lane, d = (warp - DQ_WARP0) >> 2;
-        const uint32_t t_a = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + A_COL0;
+        const uint32_t t_a = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        // Rows of x: 16-byte chunk c of a stage's 256 bytes, rows rr and rr + 8.
+        const int gt = (int)(threadIdx.x & 127), c16 = gt & 15, rr = gt >> 4;
+        const size_t pitch = (size_t)a.K * 2;
+        const uint8_t *x0 = nullptr, *x1 = nullptr, *next_x0 = nullptr, *next_x1 = nullptr;
         const uint32_t *zrow = nullptr;
-        const int nst = dep.s1 - dep.s0, packs = (nst + 1) / 2;
         // Zeros come in words of 8 groups; a stage's groups lie in one word, requested a stage of this thread ahead.
         uint32_t nz = 0;
         int nw = 0;
         auto word_of = [&](int j) { return min(((dep.s0 + j) * SK) >> lg, groups - 1) >> 3; };
-        auto rows_of = [&](const Tile &t) {
+        auto rows_of = [&](const Tile &t, int j) {   // j: this thread's first stage of tile t
             const size_t wr = min((size_t)weight_row(t, trow >> 4) + (trow & 15), (size_t)a.E * a.N - 1);
             zrow = a.qzeros + wr * zwords;
-            nw = word_of(d);
+            nw = word_of(j);
             nz = __ldg(zrow + nw);
+            // Padding repeats the last row; an index outside x reads row 0 (zeros are stored for it).
+            int v0 = t.r0 + min(rr, t.rows - 1), v1 = t.r0 + min(rr + 8, t.rows - 1);
+            if (a.rows) {
+                v0 = __ldg(a.rows + v0);
+                v1 = __ldg(a.rows + v1);
+            }
+            next_x0 = a.x + ((unsigned)v0 < (unsigned)a.T ? (size_t)v0 : 0) * pitch;
+            next_x1 = a.x + ((unsigned)v1 < (unsigned)a.T ? (size_t)v1 : 0) * pitch;
         };
-        uint32_t it0 = 0, pk0 = 0;          // ring positions of the tile's first stage and packed tile
-        bool ok = true, have = get_tile<BN, BR, 16>(a, off, tiles, first, w);
-        if (have) rows_of(w);
-        for (int t = first; ok && have; t += stride, it0 += nst, pk0 += packs) {
+        uint32_t pk0 = 0;                   // packs before this tile
+        auto first_stage = [&](uint32_t pk) { return (int)((d - 2 * pk) & 3); };
+        bool ok = true, have = get_tile<BN, BR, BR>(a, off, tiles, first, w);
+        if (have) rows_of(w, d);
+        for (int t = first; ok && have; t += stride, pk0 += packs) {
             bool ahead = false;
+            x0 = next_x0;
+            x1 = next_x1;
             auto next_tile = [&] {
-                have = get_tile<BN, BR, 16>(a, off, tiles, t + stride, w);
-                if (have) rows_of(w);
+                have = get_tile<BN, BR, BR>(a, off, tiles, t + stride, w);
+                if (have) rows_of(w, first_stage(pk0 + packs));
                 ahead = true;
             };
-            for (int j = d; j < 2 * packs; j += 4) {
+            for (int j = first_stage(pk0); j < 2 * packs; j += 4) {
                 const uint32_t pk = pk0 + (j >> 1), p = pk % P_SLOTS;
                 ok = wait_parity(smem_u32(&bar->pk_full[p]), (pk / P_SLOTS) & 1, ctl, SITE_DEQUANT);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                if (j >= nst) {   // the depth ends inside the packed tile
-                    if (lane == 0) mbar_arrive(smem_u32(&bar->pk_empty[p]));
-                    continue;
-                }
                 // 128-byte swizzle: chunk c of row r lies at c ^ (r mod 8).
                 const uint32_t pr = sP + p * P_BYTES + trow * 128;
                 uint4 v[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) v[c] = lds128(pr + (((4 * (j & 1) + c) ^ (trow & 7)) << 4));
-                const uint32_t it = it0 + j, as = it % A_STAGES;
-                ok = wait_parity(smem_u32(&bar->a_empty[as]), ((it / A_STAGES) & 1) ^ 1, ctl, SITE_DEQUANT);
+                const uint32_t it = 2 * pk0 + j, as = it % STAGES;
+                ok = wait_parity(smem_u32(&bar->empty[as]), ((it / STAGES) & 1) ^ 1, ctl, SITE_DEQUANT);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                if (j >= nst) {   // the depth ends inside the pack: an empty stage
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&bar->pk_empty[p]));
+                        mbar_arrive(smem_u32(&bar->full[as]));
+                    }
+                    continue;
+                }
                 tc_fence_after();
+                {
+                    const size_t at = (size_t)(dep.s0 + j) * (SK * 2) + c16 * 16;
+                    const bool in = at < pitch;
+                    const uint32_t dst =
+                        sX + as * X_BYTES + (c16 >> 3) * X_ATOM + rr * 128 + (((c16 ^ rr) & 7) << 4);
+                    cp_async16(dst, x0 + (in ? at : 0), in);
+                    cp_async16(dst + 8 * 128, x1 + (in ? at : 0), in);
+                    cp_async_commit();
+                }
                 const int k0 = (dep.s0 + j) * SK;
                 const uint32_t cz = nz;
                 if (j + 4 < nst) {
@@ -500,12 +477,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                     code_word<BF>(v[c].w, zc, o + 12);
                     tmem_st_32x32b_x16(t_a + as * A_COLS + c * 16, o);
                 }
+                cp_async_wait<0>();
+                fence_proxy_async_smem();
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(smem_u32(&bar->pk_empty[p]));
-                    mbar_arrive(smem_u32(&bar->a_full[as]));
+                    mbar_arrive(smem_u32(&bar->full[as]));
                 }
             }
             if (ok && !ahead) next_tile();
@@ -515,7 +494,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_before();
     __syncthreads();
     if (split > 1) cluster_sync();  // nothing of another CTA's still arrives here
-    if (warp == 2) {
+    if (warp == 3) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }

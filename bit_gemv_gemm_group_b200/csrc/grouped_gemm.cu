@@ -613,7 +613,8 @@ wq_status launch(const CUtensorMap &tx, const CUtensorMap &tw, const Args &a, lo
 }
 
 // Pair tiles once the experts have rows enough to fill them.
-bool choose_pair(const Args &a) { return (long long)a.R >= 48ll * std::min(a.E, a.R); }
+template <Kind KIND>
+bool choose_pair(const Args &a) { return (long long)a.R >= (is_w4(KIND) ? 24ll : 48ll) * std::min(a.E, a.R); }
 
 template <Kind KIND, bool PAIR>
 wq_status dispatch(const void *w, Args a, bool swiglu, cudaStream_t st, const char *who) {
@@ -646,7 +647,7 @@ wq_status run(const void *x, const void *w, Args a, bool swiglu, cudaStream_t st
     a.status = device_status_word();
     if (!a.status) return WQ_ERR_CUDA;
     a.limit_ns = wait_limit();
-    if (choose_pair(a)) return dispatch<KIND, true>(w, a, swiglu, st, who);
+    if (choose_pair<KIND>(a)) return dispatch<KIND, true>(w, a, swiglu, st, who);
     if constexpr (is_w4(KIND)) return few_rows_w4(w, a, KIND == K_W4B, swiglu, st, who);
     else return dispatch<KIND, false>(w, a, swiglu, st, who);
 }
