@@ -68,21 +68,37 @@ constexpr size_t smem_bytes(int split, int E) {
 
 static_assert(smem_bytes(MAX_SPLIT, MAX_E) <= 232448 && sizeof(Bars) <= 1024, "shared memory");
 
-// q - z of the 8 codes of a word, in k order, as fp16 or bf16 pairs.  zc: the fp16 pair -(1024 + z),
-// -(64 + z), or the bf16 pair -(128 + z) twice (see dequant_word in grouped_gemm.cu).
+// q - z of the 8 codes of a word as fp16 or bf16 pairs, in the order 0, 4, 1, 5, 2, 6, 3, 7 in which masks of
+// the word leave them (x is stored in the same order, see permute_x): the integer pipe, which runs at half
+// the issue rate, bounds this loop, and in k order each pair would take a byte permutation more.
+// fp16: masked nibbles under the exponent of 1024 read 1024 + q (low nibbles) and 1024 + 16 q (high ones).
+// bf16: 128 + q has 8 bits, so every nibble is shifted down first.
 template <bool BF>
-__device__ __forceinline__ void code_word(uint32_t w, uint32_t zc, uint32_t *o) {
-    const uint32_t w4 = w >> 4;
+struct Zero {
+    uint32_t lo, hi;   // fp16: -(1024 + z) and -(64 + z); bf16: -(128 + z)
+    __device__ __forceinline__ explicit Zero(uint32_t z)
+        : lo((BF ? 0xC300C300u : 0xE400E400u) + z * 0x00010001u), hi(0xD400D400u + z * 0x00100010u) {}
+};
+
+template <bool BF>
+__device__ __forceinline__ void code_word(uint32_t w, const Zero<BF> &z, uint32_t *o) {
+    if (BF) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (BF) {
-            const uint32_t h = (prmt(w, w4, 0x4400u + 0x1111u * i) & 0x000F000Fu) | 0x43004300u;
-            asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(h), "r"(zc));
-        } else {
-            const uint32_t h = (prmt(w, 0u, 0x4040u + 0x0101u * i) & 0x00F0000Fu) | 0x64006400u;
-            o[i] = hfma2(h, 0x2C003C00u, zc);
-        }
+        for (int i = 0; i < 4; ++i)
+            asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u), "r"(z.lo));
+    } else {
+        const uint32_t w8 = w >> 8;
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[0]) : "r"((w & 0x000F000Fu) | 0x64006400u), "r"(z.lo));
+        o[1] = hfma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, z.hi);
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[2]) : "r"((w8 & 0x000F000Fu) | 0x64006400u), "r"(z.lo));
+        o[3] = hfma2((w8 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, z.hi);
     }
+}
+
+// Eight values of x in the order of code_word.
+__device__ __forceinline__ uint4 permute_x(uint4 v) {
+    return make_uint4(prmt(v.x, v.z, 0x5410u), prmt(v.x, v.z, 0x7632u), prmt(v.y, v.w, 0x5410u),
+                      prmt(v.y, v.w, 0x7632u));
 }
 
 template <bool BF>
@@ -243,28 +259,38 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int q = warp & 3, trow = 32 * q + lane;   // TMEM lanes 32 q ..; this lane's row of the tile
         const uint32_t t_row = tmem + ((uint32_t)(32 * q) << 16);
         const int g_first = (dep.s0 * SK) >> lg, g_last = min(groups, (dep.s1 * SK + a.gs - 1) >> lg);
-        const bool vec = groups % 8 == 0;
+        const int gpp = max(1, 256 >> lg);       // groups per pack
+        const bool whole = a.K % 256 == 0;       // every pack is full, and its scales are aligned to their size
         const uint16_t *srow = nullptr;
-        uint4 ns = {}, sc = {};     // scales of 8 groups: the next window's and the current one's
+        uint4 ns = {};                           // scales of the next pack
         auto rows_of = [&](const Tile &t) {
             const size_t wr = min((size_t)weight_row(t, trow >> 4) + (trow & 15), (size_t)a.E * a.N - 1);
             srow = a.scales + wr * groups;
         };
-        auto load = [&](int b) {
-            if (vec) {
-                ns = __ldg(reinterpret_cast<const uint4 *>(srow) + b);
-            } else {
+        auto load = [&](int g) {
+            const uint16_t *p = srow + g;
+            if (!whole) {
                 uint32_t v[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = __ldg(srow + min(8 * b + i, groups - 1));
+                for (int i = 0; i < 8; ++i) v[i] = i < gpp ? __ldg(srow + min(g + i, groups - 1)) : 0u;
                 ns = make_uint4(v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16));
+            } else if (gpp == 1) {
+                ns.x = __ldg(p);
+            } else if (gpp == 2) {
+                ns.x = __ldg(reinterpret_cast<const uint32_t *>(p));
+            } else if (gpp == 4) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+                ns.x = v.x;
+                ns.y = v.y;
+            } else {
+                ns = __ldg(reinterpret_cast<const uint4 *>(p));
             }
         };
         uint32_t pk = 0, n = 0;
         bool have = get_tile<BN, BR, BR>(a, off, tiles, first, w), ok = true;
         if (have) {
             rows_of(w);
-            load(g_first >> 3);
+            load(g_first);
         }
         for (int t = first; ok && have; t += stride, ++n) {
             const Tile cur = w;
@@ -275,67 +301,51 @@ __global__ void __launch_bounds__(THREADS, 1)
             float acc[BR];
 #pragma unroll
             for (int i = 0; i < BR; ++i) acc[i] = 0.0f;
-            // Scales come in windows of 8 groups, requested one window ahead, the next tile's first at the end.
-            int win = g_first >> 3;
-            sc = ns;
-            bool ahead = false;
-            auto request = [&](int b) {
-                if (8 * b < g_last) {
-                    load(b);
+            int g = g_first;
+            for (int b = 0; b < packs; ++b, ++pk) {
+                const uint32_t c = pk % accs, cols = t_row + STAGES * A_COLS + c * acc_cols;
+                const uint4 sc = ns;
+                const int here = min(gpp, g_last - g);
+                g += gpp;
+                if (b + 1 < packs) {
+                    load(g);
                 } else {
                     have = get_tile<BN, BR, BR>(a, off, tiles, t + stride, w);
                     if (have) {
                         rows_of(w);
-                        load(g_first >> 3);
+                        load(g_first);
                     }
-                    ahead = true;
                 }
-            };
-            request(win + 1);
-            auto scale = [&](int g) {
-                if ((g >> 3) != win) {
-                    win = g >> 3;
-                    sc = ns;
-                    request(win + 1);
-                }
-                const int i = g & 7;
-                const uint32_t pr = i < 4 ? (i < 2 ? sc.x : sc.y) : (i < 6 ? sc.z : sc.w);
-                return half_bits_to_float((uint16_t)((i & 1) ? pr >> 16 : pr & 0xFFFFu));
-            };
-            int g = g_first;
-            for (int b = 0; b < packs; ++b, ++pk) {
-                const uint32_t c = pk % accs, cols = t_row + STAGES * A_COLS + c * acc_cols;
                 ok = wait_parity(smem_u32(&bar->acc_full[c]), (pk / accs) & 1, ctl, SITE_SCALE);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
-                const int end = min(g_last, g + max(1, 256 >> lg));
-                for (int i = 0; g < end; g += 2, i += 2) {   // two groups at a time
+                const uint32_t sp[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {   // two groups at a time; columns past `here` groups are not used
+                    if (2 * i >= here) break;
+                    const float2 s2 = half2_bits_to_float2(sp[i]);
                     uint32_t r[32];
-                    const bool two = g + 1 < end;
-                    if (two) {
-                        tmem_ld_32x32b_x32(cols + i * BR, r);
+                    if (gpp > 1) {
+                        tmem_ld_32x32b_x32(cols + 2 * i * BR, r);
                     } else {
                         uint32_t r1[16];
-                        tmem_ld_32x32b_x16(cols + i * BR, r1);
+                        tmem_ld_32x32b_x16(cols, r1);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) r[j] = r1[j];
                     }
-                    const float s0 = scale(g), s1 = two ? scale(g + 1) : 0.0f;
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < BR; ++j) acc[j] = fmaf(s0, __uint_as_float(r[j]), acc[j]);
-                    if (two) {
+                    for (int j = 0; j < BR; ++j) acc[j] = fmaf(s2.x, __uint_as_float(r[j]), acc[j]);
+                    if (2 * i + 1 < here) {
 #pragma unroll
-                        for (int j = 0; j < BR; ++j) acc[j] = fmaf(s1, __uint_as_float(r[16 + j]), acc[j]);
+                        for (int j = 0; j < BR; ++j) acc[j] = fmaf(s2.y, __uint_as_float(r[16 + j]), acc[j]);
                     }
                 }
-                g = end;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bar->acc_empty[c]));
             }
             if (!ok) break;
-            if (!ahead) request(INT_MAX / 8);
             if (split > 1) {
                 // Parts are added in rank order.  A lane's values lie 512 bytes apart, so that a warp's stores
                 // and loads are contiguous.
@@ -390,10 +400,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         // Group d takes every fourth stage; a thread takes one weight row of it, 128 codes.
         const int trow = 32 * (warp & 3) + lane, d = (warp - DQ_WARP0) >> 2;
         const uint32_t t_a = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        // Rows of x: 16-byte chunk c of a stage's 256 bytes, rows rr and rr + 8.
+        // Rows of x: 16-byte chunk c16 of a stage's 256 bytes, rows rr and rr + 8, requested with the zeros.
         const int gt = (int)(threadIdx.x & 127), c16 = gt & 15, rr = gt >> 4;
         const size_t pitch = (size_t)a.K * 2;
-        const uint8_t *x0 = nullptr, *x1 = nullptr, *next_x0 = nullptr, *next_x1 = nullptr;
+        const uint8_t *x0 = nullptr, *x1 = nullptr;
+        uint4 nx0 = {}, nx1 = {};
+        auto load_x = [&](int j) {
+            const size_t at = (size_t)(dep.s0 + j) * (SK * 2) + c16 * 16;
+            nx0 = nx1 = make_uint4(0, 0, 0, 0);
+            if (at < pitch) {
+                nx0 = __ldg(reinterpret_cast<const uint4 *>(x0 + at));
+                nx1 = __ldg(reinterpret_cast<const uint4 *>(x1 + at));
+            }
+        };
         const uint32_t *zrow = nullptr;
         // Zeros come in words of 8 groups; a stage's groups lie in one word, requested a stage of this thread ahead.
         uint32_t nz = 0;
@@ -410,8 +429,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 v0 = __ldg(a.rows + v0);
                 v1 = __ldg(a.rows + v1);
             }
-            next_x0 = a.x + ((unsigned)v0 < (unsigned)a.T ? (size_t)v0 : 0) * pitch;
-            next_x1 = a.x + ((unsigned)v1 < (unsigned)a.T ? (size_t)v1 : 0) * pitch;
+            x0 = a.x + ((unsigned)v0 < (unsigned)a.T ? (size_t)v0 : 0) * pitch;
+            x1 = a.x + ((unsigned)v1 < (unsigned)a.T ? (size_t)v1 : 0) * pitch;
+            load_x(j);
         };
         uint32_t pk0 = 0;                   // packs before this tile
         auto first_stage = [&](uint32_t pk) { return (int)((d - 2 * pk) & 3); };
@@ -419,8 +439,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (have) rows_of(w, d);
         for (int t = first; ok && have; t += stride, pk0 += packs) {
             bool ahead = false;
-            x0 = next_x0;
-            x1 = next_x1;
             auto next_tile = [&] {
                 have = get_tile<BN, BR, BR>(a, off, tiles, t + stride, w);
                 if (have) rows_of(w, first_stage(pk0 + packs));
@@ -446,18 +464,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                     continue;
                 }
                 tc_fence_after();
-                {
-                    const size_t at = (size_t)(dep.s0 + j) * (SK * 2) + c16 * 16;
-                    const bool in = at < pitch;
-                    const uint32_t dst =
-                        sX + as * X_BYTES + (c16 >> 3) * X_ATOM + rr * 128 + (((c16 ^ rr) & 7) << 4);
-                    cp_async16(dst, x0 + (in ? at : 0), in);
-                    cp_async16(dst + 8 * 128, x1 + (in ? at : 0), in);
-                    cp_async_commit();
-                }
+                const uint32_t xd = sX + as * X_BYTES + (c16 >> 3) * X_ATOM + rr * 128 + (((c16 ^ rr) & 7) << 4);
+                sts128(xd, permute_x(nx0));
+                sts128(xd + 8 * 128, permute_x(nx1));
+                fence_proxy_async_smem();
                 const int k0 = (dep.s0 + j) * SK;
                 const uint32_t cz = nz;
                 if (j + 4 < nst) {
+                    load_x(j + 4);
                     if (word_of(j + 4) != nw) {
                         nw = word_of(j + 4);
                         nz = __ldg(zrow + nw);
@@ -465,20 +479,21 @@ __global__ void __launch_bounds__(THREADS, 1)
                 } else {
                     next_tile();
                 }
+                const int g0 = k0 >> lg;
+                Zero<BF> z((cz >> (4 * (g0 & 7))) & 0xFu);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {   // 32 codes, all in one group
-                    const int g = min((k0 + 32 * c) >> lg, groups - 1);
-                    const uint32_t z = (cz >> (4 * (g & 7))) & 0xFu;
-                    const uint32_t zc = BF ? 0xC300C300u + z * 0x00010001u : 0xD400E400u + z * 0x00100001u;
+                    if (c > 0 && a.gs < SK) {
+                        const int g = min((k0 + 32 * c) >> lg, groups - 1);
+                        z = Zero<BF>((cz >> (4 * (g & 7))) & 0xFu);
+                    }
                     uint32_t o[16];
-                    code_word<BF>(v[c].x, zc, o);
-                    code_word<BF>(v[c].y, zc, o + 4);
-                    code_word<BF>(v[c].z, zc, o + 8);
-                    code_word<BF>(v[c].w, zc, o + 12);
+                    code_word<BF>(v[c].x, z, o);
+                    code_word<BF>(v[c].y, z, o + 4);
+                    code_word<BF>(v[c].z, z, o + 8);
+                    code_word<BF>(v[c].w, z, o + 12);
                     tmem_st_32x32b_x16(t_a + as * A_COLS + c * 16, o);
                 }
-                cp_async_wait<0>();
-                fence_proxy_async_smem();
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
