@@ -80,18 +80,32 @@ struct Zero {
         : lo((BF ? 0xC300C300u : 0xE400E400u) + z * 0x00010001u), hi(0xD400D400u + z * 0x00100010u) {}
 };
 
+// (w & mask) | magic in one LOP3: `magic` comes from a register that the compiler cannot fold into a second one.
+__device__ __forceinline__ uint32_t mask_or(uint32_t w, uint32_t mask, uint32_t magic) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
+    return d;
+}
+
 template <bool BF>
-__device__ __forceinline__ void code_word(uint32_t w, const Zero<BF> &z, uint32_t *o) {
+__device__ __forceinline__ uint32_t code_magic() {
+    uint32_t m;
+    asm volatile("mov.b32 %0, %1;" : "=r"(m) : "n"(BF ? 0x43004300 : 0x64006400));
+    return m;
+}
+
+template <bool BF>
+__device__ __forceinline__ void code_word(uint32_t w, uint32_t magic, const Zero<BF> &z, uint32_t *o) {
     if (BF) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u), "r"(z.lo));
+            asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(mask_or(w >> (4 * i), 0x000F000Fu, magic)), "r"(z.lo));
     } else {
         const uint32_t w8 = w >> 8;
-        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[0]) : "r"((w & 0x000F000Fu) | 0x64006400u), "r"(z.lo));
-        o[1] = hfma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, z.hi);
-        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[2]) : "r"((w8 & 0x000F000Fu) | 0x64006400u), "r"(z.lo));
-        o[3] = hfma2((w8 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, z.hi);
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[0]) : "r"(mask_or(w, 0x000F000Fu, magic)), "r"(z.lo));
+        o[1] = hfma2(mask_or(w, 0x00F000F0u, magic), 0x2C002C00u, z.hi);
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[2]) : "r"(mask_or(w8, 0x000F000Fu, magic)), "r"(z.lo));
+        o[3] = hfma2(mask_or(w8, 0x00F000F0u, magic), 0x2C002C00u, z.hi);
     }
 }
 
@@ -433,6 +447,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             x1 = a.x + ((unsigned)v1 < (unsigned)a.T ? (size_t)v1 : 0) * pitch;
             load_x(j);
         };
+        const uint32_t magic = code_magic<BF>();
         uint32_t pk0 = 0;                   // packs before this tile
         auto first_stage = [&](uint32_t pk) { return (int)((d - 2 * pk) & 3); };
         bool ok = true, have = get_tile<BN, BR, BR>(a, off, tiles, first, w);
@@ -488,10 +503,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         z = Zero<BF>((cz >> (4 * (g & 7))) & 0xFu);
                     }
                     uint32_t o[16];
-                    code_word<BF>(v[c].x, z, o);
-                    code_word<BF>(v[c].y, z, o + 4);
-                    code_word<BF>(v[c].z, z, o + 8);
-                    code_word<BF>(v[c].w, z, o + 12);
+                    code_word<BF>(v[c].x, magic, z, o);
+                    code_word<BF>(v[c].y, magic, z, o + 4);
+                    code_word<BF>(v[c].z, magic, z, o + 8);
+                    code_word<BF>(v[c].w, magic, z, o + 12);
                     tmem_st_32x32b_x16(t_a + as * A_COLS + c * 16, o);
                 }
                 tmem_st_wait();
