@@ -90,6 +90,19 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     return d;
 }
 
+// (w & mask) | magic in one LOP3: `magic` comes from opaque_const, which the compiler cannot fold into a second one.
+__device__ __forceinline__ uint32_t mask_or(uint32_t w, uint32_t mask, uint32_t magic) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t opaque_const(uint32_t v) {
+    uint32_t m;
+    asm volatile("mov.b32 %0, %1;" : "=r"(m) : "r"(v));
+    return m;
+}
+
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));

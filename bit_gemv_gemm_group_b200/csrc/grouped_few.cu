@@ -80,20 +80,6 @@ struct Zero {
         : lo((BF ? 0xC300C300u : 0xE400E400u) + z * 0x00010001u), hi(0xD400D400u + z * 0x00100010u) {}
 };
 
-// (w & mask) | magic in one LOP3: `magic` comes from a register that the compiler cannot fold into a second one.
-__device__ __forceinline__ uint32_t mask_or(uint32_t w, uint32_t mask, uint32_t magic) {
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
-    return d;
-}
-
-template <bool BF>
-__device__ __forceinline__ uint32_t code_magic() {
-    uint32_t m;
-    asm volatile("mov.b32 %0, %1;" : "=r"(m) : "n"(BF ? 0x43004300 : 0x64006400));
-    return m;
-}
-
 template <bool BF>
 __device__ __forceinline__ void code_word(uint32_t w, uint32_t magic, const Zero<BF> &z, uint32_t *o) {
     if (BF) {
@@ -447,7 +433,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             x1 = a.x + ((unsigned)v1 < (unsigned)a.T ? (size_t)v1 : 0) * pitch;
             load_x(j);
         };
-        const uint32_t magic = code_magic<BF>();
+        const uint32_t magic = opaque_const(BF ? 0x43004300u : 0x64006400u);
         uint32_t pk0 = 0;                   // packs before this tile
         auto first_stage = [&](uint32_t pk) { return (int)((d - 2 * pk) & 3); };
         bool ok = true, have = get_tile<BN, BR, BR>(a, off, tiles, first, w);

@@ -26,7 +26,7 @@
 //   warp 2      allocates tensor memory
 //   warp 3      (INT4) packed weight tiles, 128 rows x 128 bytes (four stages), into a ring of their own:
 //               with 32-byte rows a TMA request took about 1000 cycles for its 4 KB
-//   warps 4-7   epilogue of the previous tile: scales, SwiGLU, conversion, stores
+//   warps 4-7   epilogue of the previous tile: scales, SwiGLU, conversion, stores (4-11 for 8-bit pairs)
 //   then        four warps that gather indexed activation rows by cp.async (TMA's gather of four rows a
 //               request took 32 cycles for its 512 bytes, four times what the MMAs leave), and for INT4
 //               four groups of four warps that dequantize every fourth stage each
@@ -48,15 +48,15 @@ constexpr uint32_t A_BYTES = BM * STAGE_K;
 constexpr int PK = 4;                  // stages per packed INT4 tile (128 bytes of a weight row)
 constexpr uint32_t P_BYTES = BM * PK * 32;
 constexpr int EPI_WARP0 = 4, GATHER_WARPS = 4, DQ_GROUPS = 4;
-constexpr int LAG = 2;                 // stages of gathered rows in flight per thread
 constexpr int MAX_STAGES = 8, MAX_PSTAGES = 3;
 constexpr unsigned SITE_PRODUCER = 0x1001, SITE_MMA = 0x1002, SITE_EPILOGUE = 0x1004, SITE_DRAIN = 0x1008,
                    SITE_DEQUANT = 0x1010, SITE_PACKED = 0x1020, SITE_GATHER = 0x1040;
 
 struct Bars {
     uint64_t full[MAX_STAGES], empty[MAX_STAGES];  // TMA copies of a stage landed / its MMAs done
-    uint64_t put[MAX_STAGES];  // what warps write of a stage: gathered rows and dequantized weights (an arrival
-                               // per warp) and, in a pair's first CTA, word that the second's share is there
+    uint64_t put[MAX_STAGES];  // what warps write of a stage: gathered rows (an arrival per thread, when its
+                               // copies land), dequantized weights (one per warp) and, in a pair's first CTA,
+                               // word that the second's share is there
     uint64_t pk_full[MAX_PSTAGES], pk_empty[MAX_PSTAGES];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
@@ -75,19 +75,20 @@ struct Layout {
     static constexpr int STAGES = PAIR ? (W4 ? 5 : 6) : 8;
     static constexpr int PSTAGES = 3;                        // packed INT4 tiles
     static constexpr int BOX = PAIR ? 64 : 16;               // rows per box when the activations lie in order
-    static constexpr int GA_WARP0 = 8;
+    static constexpr int EPI_WARPS = PAIR && !W4 ? 8 : 4;    // 8: two per 32 TMEM lanes, half the rows each
+    static constexpr int GA_WARP0 = EPI_WARP0 + EPI_WARPS;
     static constexpr int DQ_WARP0 = GA_WARP0 + (GATHER ? GATHER_WARPS : 0);
     static constexpr int THREADS = 32 * (DQ_WARP0 + (W4 ? 4 * DQ_GROUPS : 0));
     static constexpr uint32_t OFF_B = STAGES * A_BYTES;
     static constexpr uint32_t OFF_P = OFF_B + STAGES * B_BYTES;
     static constexpr uint32_t OFF_BAR = OFF_P + (W4 ? PSTAGES * P_BYTES : 0);
-    static constexpr uint32_t OFF_SRC = OFF_BAR + 1024;                   // int [2][BR]: token of each row
-    static constexpr uint32_t OFF_SX = OFF_SRC + 2 * BR * 4;              // float [2][BR] (8-bit kinds)
+    static constexpr uint32_t OFF_SRC = OFF_BAR + 1024;                   // bits [2][BR]: rows whose index is bad
+    static constexpr uint32_t OFF_SX = OFF_SRC + (GATHER ? 2 * BR / 8 : 0);  // float [2][BR] (8-bit kinds)
     static constexpr uint32_t OFF_TAB = OFF_SX + (W4 ? 0 : 2 * BR * 4);   // int offsets[E + 1], tiles[E + 1]
     static constexpr size_t smem(int E) { return 1024 + OFF_TAB + 2 * (size_t)(E + 1) * 4; }
     static_assert(PAIR || !W4, "INT4 with few rows has a kernel of its own");
     static_assert(smem(MAX_E) <= 232448, "fits the shared memory of a CTA");
-    static_assert(STAGES <= MAX_STAGES && PSTAGES <= MAX_PSTAGES && STAGES > LAG, "barrier arrays, gather lag");
+    static_assert(STAGES <= MAX_STAGES && PSTAGES <= MAX_PSTAGES, "barrier arrays");
 };
 static_assert(sizeof(Bars) <= 1024, "barriers fit their space");
 
@@ -145,17 +146,17 @@ struct GroupConst {
 // bf16: 128 + q has 8 bits, so a nibble can only sit in the lowest bits: the odd codes come from the word
 // shifted by 4.  (q - z) hi + (q - z) lo in one fma after a product whose own rounding is 2^-16 of the result.
 template <bool BF>
-__device__ __forceinline__ uint4 dequant_word(uint32_t w, const GroupConst<BF> &g) {
+__device__ __forceinline__ uint4 dequant_word(uint32_t w, uint32_t magic, const GroupConst<BF> &g) {
     uint32_t o[4];
     const uint32_t w4 = w >> 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (BF) {
-            const uint32_t h = (prmt(w, w4, 0x4400u + 0x1111u * i) & 0x000F000Fu) | 0x43004300u;
+            const uint32_t h = mask_or(prmt(w, w4, 0x4400u + 0x1111u * i), 0x000F000Fu, magic);
             const uint32_t d = bfma2(h, 0x3F803F80u, g.zc);
             o[i] = bfma2(d, g.hi, bfma2(d, g.lo, 0x80008000u));
         } else {
-            const uint32_t h = (prmt(w, 0u, 0x4040u + 0x0101u * i) & 0x00F0000Fu) | 0x64006400u;
+            const uint32_t h = mask_or(prmt(w, 0u, 0x4040u + 0x0101u * i), 0x00F0000Fu, magic);
             o[i] = hmul2(hfma2(h, 0x2C003C00u, g.zc), g.hi);
         }
     }
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Bars *bar = reinterpret_cast<Bars *>(base + L::OFF_BAR);
-    int *src_tab = reinterpret_cast<int *>(base + L::OFF_SRC);
+    uint32_t *bad_tab = reinterpret_cast<uint32_t *>(base + L::OFF_SRC);
     float *sx_tab = reinterpret_cast<float *>(base + L::OFF_SX);
     int *off = reinterpret_cast<int *>(base + L::OFF_TAB), *tiles = off + a.E + 1;
     const uint32_t sA = smem_u32(base), sB = smem_u32(base + L::OFF_B), sP = smem_u32(base + L::OFF_P);
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&bar->full[s]), 1);
             mbar_init(smem_u32(&bar->empty[s]), 1);
-            mbar_init(smem_u32(&bar->put[s]), max(1, (GATHER ? GATHER_WARPS : 0) + (W4 ? 4 : 0) + (PAIR && rank == 0)));
+            mbar_init(smem_u32(&bar->put[s]), max(1, (GATHER ? 32 * GATHER_WARPS : 0) + (W4 ? 4 : 0) + (PAIR && rank == 0)));
         }
         for (int p = 0; p < PSTAGES; ++p) {
             mbar_init(smem_u32(&bar->pk_full[p]), 1);
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bar->acc_full[i]), 1);
-            mbar_init(smem_u32(&bar->acc_empty[i]), PAIR ? 8 : 4);
+            mbar_init(smem_u32(&bar->acc_empty[i]), (PAIR ? 2 : 1) * L::EPI_WARPS);
         }
         mbar_init(smem_u32(&bar->drain), 1);
         bar->abort = 0;
@@ -301,6 +302,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                      (!(rank == 0 ? PUT0 : PUT1) || wait_parity(smem_u32(&bar->put[s]), ph, ctl, SITE_MMA));
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
+                if (GATHER) fence_proxy_async_smem();  // rows copied by cp.async, read by the tensor cores
                 if (leader) {
                     if (rank == 0) {
                         const uint64_t da = desc_a + s * (A_BYTES >> 4), db = desc_b + s * (L::B_BYTES >> 4);
@@ -354,27 +356,35 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
             if (issued) drain_parity(smem_u32(&bar->pk_full[p]), (issued - 1) & 1, DRAIN_NS, a.status, SITE_DRAIN);
         }
         __syncwarp();
-    } else if (warp >= EPI_WARP0 && warp < EPI_WARP0 + 4) {
+    } else if (warp >= EPI_WARP0 && warp < EPI_WARP0 + L::EPI_WARPS) {
         // -------------------------------------------------------------------- epilogue
         const int q = warp & 3;                   // TMEM lanes 32 q .. 32 q + 31
-        const int et = (int)threadIdx.x - 32 * EPI_WARP0;
+        constexpr int PARTS = L::EPI_WARPS / 4, ET = 32 * L::EPI_WARPS;
+        const int part = (warp - EPI_WARP0) >> 2; // takes every PARTS-th 32 rows
         const uint32_t t_row = tmem_base + ((uint32_t)(32 * q) << 16);
         uint32_t n = 0;
         bool ok = true;
         for (int t = first; get_tile<BN, BR, STEP>(a, off, tiles, t, w); t += stride, ++n) {
             const uint32_t acc = n & 1, u = n >> 1;
-            int *src = src_tab + acc * BR;
+            uint32_t *bad = bad_tab + acc * (BR / 32);
             float *sxs = sx_tab + acc * BR;
-            for (int r = et; r < w.rows; r += 128) {
-                int v = w.r0 + r;
-                if (GATHER) {
-                    v = __ldg(a.rows + v);
-                    if ((unsigned)v >= (unsigned)a.T) v = -1;
+            if (GATHER || !W4) {
+                for (int r0 = 32 * (warp - EPI_WARP0); r0 < w.rows; r0 += ET) {
+                    const int r = r0 + lane;
+                    int v = w.r0 + r;
+                    bool out = false;
+                    if (GATHER && r < w.rows) {
+                        v = __ldg(a.rows + v);
+                        out = (unsigned)v >= (unsigned)a.T;
+                    }
+                    if (GATHER) {
+                        const uint32_t m = __ballot_sync(0xffffffffu, out);
+                        if (lane == 0) bad[r0 / 32] = m;
+                    }
+                    if (!W4) sxs[r] = r < w.rows && !out ? __ldg(a.sx + (size_t)v * a.sx_stride) : 0.0f;
                 }
-                src[r] = v;
-                if (!W4) sxs[r] = v >= 0 ? __ldg(a.sx + (size_t)v * a.sx_stride) : 0.0f;
+                asm volatile("bar.sync 1, %0;" ::"n"(ET) : "memory");
             }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
             const int col = w.n0 + rank * BNC + (SWIGLU ? 16 * q + (lane & 15) : 32 * q + lane);
             const bool col_ok = col < a.ldy;
             float sw = 1.0f;
@@ -382,37 +392,55 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                 sw = a.sw_per_row ? __ldg(a.sw + min((size_t)a.E * a.N - 1,
                                                      (size_t)weight_row(w, 2 * q + (lane >> 4)) + (lane & 15)))
                                   : __ldg(a.sw + w.e);
-            // After a wait has run out the warps still walk the tiles, so that all four meet at the barrier.
+            // After a wait has run out the warps still walk the tiles, so that all meet at the barrier.
             ok = ok && wait_parity(smem_u32(&bar->acc_full[acc]), u & 1, ctl, SITE_EPILOGUE);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) continue;
             tc_fence_after();
-            uint16_t *yt = a.y + (size_t)w.r0 * a.ldy;
-            for (int c = 0; c < w.rows; c += 16) {
-                uint32_t r[16];
-                tmem_ld_32x32b_x16(t_row + acc * BR + c, r);
+            for (int c = 32 * part; c < w.rows; c += 32 * PARTS) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(t_row + acc * BR + c, r);
                 tmem_ld_wait();
-                float v[16];
+                const uint32_t zero = GATHER ? bad[c / 32] : 0u;
+                const int left = w.rows - c;
+                uint16_t *yt = a.y + (size_t)(w.r0 + c) * a.ldy + col;
+                // Values in place of the accumulators, scaled.
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float f = KIND == K_I8 ? (float)(int32_t)r[j] : __uint_as_float(r[j]);
-                    v[j] = W4 ? f : __fmul_rn(__fmul_rn(f, sxs[min(c + j, w.rows - 1)]), sw);
+                for (int j = 0; j < 32; j += 4) {
+                    if (W4) continue;
+                    const float4 sx = *reinterpret_cast<const float4 *>(sxs + c + j);
+                    const float sv[4] = {sx.x, sx.y, sx.z, sx.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float f = KIND == K_I8 ? (float)(int32_t)r[j + i] : __uint_as_float(r[j + i]);
+                        r[j + i] = __float_as_uint(__fmul_rn(__fmul_rn(f, sv[i]), sw));
+                    }
                 }
                 if (SWIGLU) {
-                    const bool up = lane >= 16;   // this lane's weight row is an up row
+                    // Lanes 0-15 hold gate rows and keep the even rows of y, lanes 16-31 up rows and the odd ones.
+                    const bool up = lane >= 16;
+                    yt += up ? a.ldy : 0;
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float other = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 16);
-                        const float g = up ? other : v[j], l = up ? v[j + 1] : other;
-                        const int row = c + j + (up ? 1 : 0);
-                        if (row < w.rows && col_ok)
-                            yt[(size_t)row * a.ldy + col] = src[row] >= 0 ? out_bits<KIND>(swiglu(g, l)) : (uint16_t)0;
+                    for (int j = 0; j < 32; j += 2) {
+                        const uint32_t other = __shfl_xor_sync(0xffffffffu, up ? r[j] : r[j + 1], 16);
+                        const float g = __uint_as_float(up ? other : r[j]), l = __uint_as_float(up ? r[j + 1] : other);
+                        r[j] = out_bits<KIND>(swiglu(g, l));
                     }
-                } else {
+                    if (zero)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c + j < w.rows && col_ok)
-                            yt[(size_t)(c + j) * a.ldy + col] = src[c + j] >= 0 ? out_bits<KIND>(v[j]) : (uint16_t)0;
+                        for (int j = 0; j < 32; j += 2)
+                            if ((zero >> (j + (up ? 1 : 0))) & 1) r[j] = 0;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2)
+                        if (j + (up ? 1 : 0) < left && col_ok) yt[(size_t)j * a.ldy] = (uint16_t)r[j];
+                } else {
+                    if (zero)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if ((zero >> j) & 1) r[j] = 0;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j < left && col_ok) yt[(size_t)j * a.ldy] = out_bits<KIND>(__uint_as_float(r[j]));
                 }
             }
             tc_fence_before();
@@ -425,7 +453,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
     } else if (GATHER && warp >= L::GA_WARP0 && warp < L::GA_WARP0 + GATHER_WARPS) {
         // -------------------------------------------------------------------- gathered activations
         // Thread (16-byte chunk c of a row's 128 bytes, row rr of every 16): cp.async into the 128-byte
-        // swizzle, LAG stages in flight.  Padding repeats the last row; an index outside x reads row 0 (the
+        // swizzle, whose completion arrives on the stage's barrier by itself.  Padding repeats the last row; an index outside x reads row 0 (the
         // epilogue writes zeros for it).
         constexpr int PASSES = L::SR / 16;
         const int gt = (int)threadIdx.x - 32 * L::GA_WARP0, c = gt & 7, rr = gt >> 3;
@@ -433,11 +461,6 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
         const uint32_t dst0 = sB + rr * STAGE_K + ((c ^ (rr & 7)) << 4);
         uint32_t it = 0;
         bool ok = true;
-        auto signal = [&](uint32_t i) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bar->put[i % STAGES]));
-        };
         for (int t = first; ok && get_tile<BN, BR, STEP>(a, off, tiles, t, w); t += stride) {
             const int mine = local_rows(w);
             const uint8_t *src[PASSES];
@@ -456,21 +479,16 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                 for (int j = 0; j < PASSES; ++j)
                     if (16 * j < mine)
                         cp_async16(dst0 + s * L::B_BYTES + 16 * j * STAGE_K, src[j] + (in ? at : 0), in);
-                cp_async_commit();
-                if (it >= LAG) {
-                    cp_async_wait<LAG>();
-                    signal(it - LAG);
-                }
+                cp_async_arrive(smem_u32(&bar->put[s]));
             }
         }
-        cp_async_wait<0>();
-        if (ok)
-            for (uint32_t i = it > LAG ? it - LAG : 0; i < it; ++i) signal(i);
+        cp_async_wait_all();
     } else if (W4 && warp >= L::DQ_WARP0) {
         // -------------------------------------------------------------------- dequantizers
         // Group g of four warps takes the g-th stage of every packed tile; a thread takes one weight row of it,
         // 64 codes.
         constexpr bool BF = KIND == K_W4B;
+        const uint32_t magic = opaque_const(BF ? 0x43004300u : 0x64006400u);
         const int row = 32 * (warp & 3) + lane;
         const uint32_t group = (uint32_t)(warp - L::DQ_WARP0) >> 2;
         const int lg = 31 - __clz(a.gs), groups = a.K >> lg, zwords = (groups + 7) / 8;
@@ -555,10 +573,10 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                 GroupConst<BF> c = constants(g0);
                 const uint32_t w0[4] = {q0.x, q0.y, q0.z, q0.w}, w1[4] = {q1.x, q1.y, q1.z, q1.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sts128(dst + ((j ^ (row & 7)) << 4), dequant_word<BF>(w0[j], c));
+                for (int j = 0; j < 4; ++j) sts128(dst + ((j ^ (row & 7)) << 4), dequant_word<BF>(w0[j], magic, c));
                 if (g1 != g0) c = constants(g1);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sts128(dst + (((4 + j) ^ (row & 7)) << 4), dequant_word<BF>(w1[j], c));
+                for (int j = 0; j < 4; ++j) sts128(dst + (((4 + j) ^ (row & 7)) << 4), dequant_word<BF>(w1[j], magic, c));
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
