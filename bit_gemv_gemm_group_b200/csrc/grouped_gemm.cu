@@ -467,18 +467,19 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
 #pragma unroll
             for (int j = 0; j < PASSES; ++j) {
                 const int v = __ldg(a.rows + w.r0 + min(rank * mine + 16 * j + rr, w.rows - 1));
-                src[j] = a.x + ((unsigned)v < (unsigned)a.T ? (size_t)v : 0) * pitch;
+                src[j] = a.x + ((unsigned)v < (unsigned)a.T ? (size_t)v : 0) * pitch + c * 16;
             }
             for (int kb = 0; kb < kst; ++kb, ++it) {
                 const uint32_t s = it % STAGES, u = it / STAGES;
                 ok = wait_parity(smem_u32(&bar->empty[s]), (u & 1) ^ 1, ctl, SITE_GATHER);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                const size_t at = (size_t)kb * STAGE_K + c * 16;
-                const bool in = at < pitch;
+                const uint32_t dst = dst0 + s * L::B_BYTES;
+                const bool in = kb * STAGE_K + c * 16 < (int)pitch;   // false only past the end of the depth
 #pragma unroll
-                for (int j = 0; j < PASSES; ++j)
-                    if (16 * j < mine)
-                        cp_async16(dst0 + s * L::B_BYTES + 16 * j * STAGE_K, src[j] + (in ? at : 0), in);
+                for (int j = 0; j < PASSES; ++j) {
+                    if (16 * j < mine) cp_async16(dst + 16 * j * STAGE_K, in ? src[j] : a.x, in);
+                    src[j] += STAGE_K;
+                }
                 cp_async_arrive(smem_u32(&bar->put[s]));
             }
         }
