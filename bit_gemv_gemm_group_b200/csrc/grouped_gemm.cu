@@ -514,7 +514,9 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                 ns = make_uint4(v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16));
             }
         };
-        uint32_t it0 = 0, pt = 0; // ring positions of the tile's first stage and of the packed tile
+        uint32_t it0 = 0;         // stages before the tile
+        uint32_t p = 0, pp = 0;   // slot and phase parity of the packed tile
+        const uint32_t r7 = (uint32_t)(row & 7) << 4, in_row = sP + row * STAGE_K, out_row = sA + row * STAGE_K;
         bool ok = true, have = get_tile<BN, BR, STEP>(a, off, tiles, first, w);
         if (have) {
             rows_of(w);
@@ -540,16 +542,24 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                 }
             };
             request(1);
-            for (int b = 0; b < packs; ++b, ++pt) {
-                const uint32_t p = pt % PSTAGES;
-                const int kb = b * PK + (int)group;
-                ok = wait_parity(smem_u32(&bar->pk_full[p]), (pt / PSTAGES) & 1, ctl, SITE_DEQUANT);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            uint32_t st = (it0 + group) % STAGES, sp = ((it0 + group) / STAGES) & 1;   // this group's stage slot
+            for (int kb = (int)group; kb < packs * PK; kb += PK) {
+                const uint32_t pf = smem_u32(&bar->pk_full[p]), pe = smem_u32(&bar->pk_empty[p]);
                 if (kb >= kst) {  // the tile's depth ends inside the packed tile
-                    if (lane == 0) mbar_arrive(smem_u32(&bar->pk_empty[p]));
+                    ok = wait_parity(pf, pp, ctl, SITE_DEQUANT);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (lane == 0) mbar_arrive(pe);
+                    if (++p == PSTAGES) {
+                        p = 0;
+                        pp ^= 1;
+                    }
                     continue;
                 }
-                const uint32_t it = it0 + kb, s = it % STAGES, us = it / STAGES;
+                ok = wait_parity2(pf, pp, smem_u32(&bar->empty[st]), sp ^ 1, ctl, SITE_DEQUANT);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                // 128-byte swizzle: chunk c of row r lies at c ^ (r mod 8).
+                const uint32_t src = in_row + p * P_BYTES, dst = out_row + st * A_BYTES;
+                const uint4 q0 = lds128(src + ((2 * group << 4) ^ r7)), q1 = lds128(src + (((2 * group + 1) << 4) ^ r7));
                 const int g0 = min((kb * KE) >> lg, groups - 1), g1 = min((kb * KE + 32) >> lg, groups - 1);
                 if ((g0 >> 3) != win) {
                     win = g0 >> 3;
@@ -564,26 +574,27 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                     c.set((i & 1) ? pr >> 16 : pr & 0xFFFFu, (cz >> (4 * i)) & 0xFu);
                     return c;
                 };
-                // 128-byte swizzle: chunk c of row r lies at c ^ (r mod 8).
-                const uint32_t pr = sP + p * P_BYTES + row * STAGE_K;
-                const uint4 q0 = lds128(pr + (((2 * group) ^ (row & 7)) << 4));
-                const uint4 q1 = lds128(pr + (((2 * group + 1) ^ (row & 7)) << 4));
-                ok = wait_parity(smem_u32(&bar->empty[s]), (us & 1) ^ 1, ctl, SITE_DEQUANT);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                const uint32_t dst = sA + s * A_BYTES + row * STAGE_K;
                 GroupConst<BF> c = constants(g0);
                 const uint32_t w0[4] = {q0.x, q0.y, q0.z, q0.w}, w1[4] = {q1.x, q1.y, q1.z, q1.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sts128(dst + ((j ^ (row & 7)) << 4), dequant_word<BF>(w0[j], magic, c));
+                for (int j = 0; j < 4; ++j) sts128(dst + ((j << 4) ^ r7), dequant_word<BF>(w0[j], magic, c));
                 if (g1 != g0) c = constants(g1);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sts128(dst + (((4 + j) ^ (row & 7)) << 4), dequant_word<BF>(w1[j], magic, c));
+                for (int j = 0; j < 4; ++j) sts128(dst + (((4 + j) << 4) ^ r7), dequant_word<BF>(w1[j], magic, c));
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(smem_u32(&bar->pk_empty[p]));
-                    mbar_arrive(smem_u32(&bar->put[s]));
+                    mbar_arrive(pe);
+                    mbar_arrive(smem_u32(&bar->put[st]));
                 }
+                if (++p == PSTAGES) {
+                    p = 0;
+                    pp ^= 1;
+                }
+                // Four stages on: the slot before this one, of the next round of the ring unless this is slot 0.
+                static_assert(!W4 || STAGES == PK + 1, "ring step");
+                sp ^= st > 0;
+                st = st > 0 ? st - 1 : STAGES - 1;
             }
             if (ok && !ahead) {
                 have = get_tile<BN, BR, STEP>(a, off, tiles, t + stride, w);
