@@ -19,8 +19,9 @@
 //   warps 4-7    scale: each pack's accumulators, times the scales of the lane's weight row, into registers;
 //                at the end of a tile the cluster's parts meet in the first CTA's shared memory, which
 //                applies SwiGLU, rounds and stores
-//   warps 8-23   four groups of four warps, every fourth stage (half a pack) each: rows of x by cp.async, and
-//                codes -> q - z into tensor memory
+//   warps 8-15   two groups of four warps, every other pack each: rows of x into shared memory, and codes ->
+//                q - z into tensor memory.  A thread takes 256 codes at a time: with 128 (and twice the warps)
+//                its waits, loads and addresses were 250 of 390 instructions
 #include "grouped.cuh"
 
 #include <algorithm>
@@ -38,7 +39,7 @@ constexpr int STAGES = 4, P_SLOTS = 8, MAX_ACCS = 8;
 constexpr uint32_t X_ATOM = BR * 128, X_BYTES = 2 * X_ATOM;   // 64 values a row and atom
 constexpr uint32_t P_BYTES = BM * 128;      // a pack: 256 codes of 128 rows, two stages
 constexpr uint32_t A_COLS = SK / 2;         // tensor memory columns of a stage
-constexpr int THREADS = 768, SCALE_WARP0 = 4, DQ_WARP0 = 8;
+constexpr int THREADS = 512, SCALE_WARP0 = 4, DQ_WARP0 = 8;
 constexpr int MAX_SPLIT = 4;
 constexpr uint32_t OFF_X = P_SLOTS * P_BYTES;
 constexpr uint32_t OFF_RED = OFF_X + STAGES * X_BYTES;    // not used when the tile is not split
@@ -47,8 +48,8 @@ constexpr unsigned SITE_PACKED = 0x2001, SITE_MMA = 0x2002, SITE_SCALE = 0x2008,
                    SITE_DRAIN = 0x2020, SITE_SPLIT = 0x2040;
 
 // Tensor memory: four stages of 64 columns, then accumulators, 16 columns per group and 256 / gs groups per pack.
-// Stage and accumulator slots belong to one dequantizing group and one issuer each (4 stages, an even number
-// of accumulators): a thread that waited for a slot another one had not used yet could take an older phase of
+// Pack, stage and accumulator slots belong to one dequantizing group and one issuer each (an even number of
+// packs, 4 stages, an even number of accumulators): a thread that waited for a slot another one had not used yet could take an older phase of
 // its barrier, of the same parity, for the one it waits for.
 static_assert(STAGES * A_COLS + 256 * BR / 16 <= 512, "tensor memory");
 
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < P_SLOTS; ++i) {
             mbar_init(smem_u32(&bar->pk_full[i]), 1);
-            mbar_init(smem_u32(&bar->pk_empty[i]), 8);
+            mbar_init(smem_u32(&bar->pk_empty[i]), 4);
         }
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(smem_u32(&bar->full[i]), 4);
@@ -397,113 +398,111 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else {
         // -------------------------------------------------------------------- codes -> q - z
-        // Group d takes every fourth stage; a thread takes one weight row of it, 128 codes.
-        const int trow = 32 * (warp & 3) + lane, d = (warp - DQ_WARP0) >> 2;
-        const uint32_t t_a = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        // Rows of x: 16-byte chunk c16 of a stage's 256 bytes, rows rr and rr + 8, requested with the zeros.
-        const int gt = (int)(threadIdx.x & 127), c16 = gt & 15, rr = gt >> 4;
-        const size_t pitch = (size_t)a.K * 2;
-        const uint8_t *x0 = nullptr, *x1 = nullptr;
-        uint4 nx0 = {}, nx1 = {};
-        auto load_x = [&](int j) {
-            const size_t at = (size_t)(dep.s0 + j) * (SK * 2) + c16 * 16;
-            nx0 = nx1 = make_uint4(0, 0, 0, 0);
-            if (at < pitch) {
-                nx0 = __ldg(reinterpret_cast<const uint4 *>(x0 + at));
-                nx1 = __ldg(reinterpret_cast<const uint4 *>(x1 + at));
-            }
-        };
-        const uint32_t *zrow = nullptr;
-        // Zeros come in words of 8 groups; a stage's groups lie in one word, requested a stage of this thread ahead.
-        uint32_t nz = 0;
-        int nw = 0;
-        auto word_of = [&](int j) { return min(((dep.s0 + j) * SK) >> lg, groups - 1) >> 3; };
-        auto rows_of = [&](const Tile &t, int j) {   // j: this thread's first stage of tile t
-            const size_t wr = min((size_t)weight_row(t, trow >> 4) + (trow & 15), (size_t)a.E * a.N - 1);
-            zrow = a.qzeros + wr * zwords;
-            nw = word_of(j);
-            nz = __ldg(zrow + nw);
-            // Padding repeats the last row; an index outside x reads row 0 (zeros are stored for it).
-            int v0 = t.r0 + min(rr, t.rows - 1), v1 = t.r0 + min(rr + 8, t.rows - 1);
-            if (a.rows) {
-                v0 = __ldg(a.rows + v0);
-                v1 = __ldg(a.rows + v1);
-            }
-            x0 = a.x + ((unsigned)v0 < (unsigned)a.T ? (size_t)v0 : 0) * pitch;
-            x1 = a.x + ((unsigned)v1 < (unsigned)a.T ? (size_t)v1 : 0) * pitch;
-            load_x(j);
-        };
+        // Group d takes every other pack and fills stages 2 d and 2 d + 1; a thread takes one weight row.
+        const int q = warp & 3, trow = 32 * q + lane, d = (warp - DQ_WARP0) >> 2;
+        const uint32_t t_a = tmem + ((uint32_t)(32 * q) << 16) + 2 * d * A_COLS, r7 = (uint32_t)(trow & 7) << 4;
         const uint32_t magic = opaque_const(BF ? 0x43004300u : 0x64006400u);
+        const uint32_t fb = smem_u32(&bar->full[2 * d]), eb = smem_u32(&bar->empty[2 * d]);
+        // Rows of x: warp q brings rows q, q + 4, q + 8, q + 12 of the tile, a lane 16 of the pack's 512 bytes.
+        const size_t pitch = (size_t)a.K * 2;
+        const uint32_t xd = sX + (2 * d + (lane >> 4)) * X_BYTES + ((lane >> 3) & 1) * X_ATOM;
+        const uint8_t *xp[4] = {};
+        const uint32_t *zrow = nullptr;
+        uint4 nx[4] = {};                   // x and zeros of this thread's next pack
+        uint32_t nz = 0;
+        int rows = 0;                       // of the tile that they belong to
+        auto load = [&](int b) {            // pack b of the tile whose pointers are set
+            const int k0 = (dep.s0 + 2 * b) * SK;
+            nz = __ldg(zrow + (min(k0 >> lg, groups - 1) >> 3));
+            const size_t at = (size_t)k0 * 2 + lane * 16;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (q + 4 * i < rows)
+                    nx[i] = at < pitch ? __ldg(reinterpret_cast<const uint4 *>(xp[i] + at)) : make_uint4(0, 0, 0, 0);
+        };
         uint32_t pk0 = 0;                   // packs before this tile
-        auto first_stage = [&](uint32_t pk) { return (int)((d - 2 * pk) & 3); };
-        bool ok = true, have = get_tile<BN, BR, BR>(a, off, tiles, first, w);
-        if (have) rows_of(w, d);
-        for (int t = first; ok && have; t += stride, pk0 += packs) {
-            bool ahead = false;
-            auto next_tile = [&] {
-                have = get_tile<BN, BR, BR>(a, off, tiles, t + stride, w);
-                if (have) rows_of(w, first_stage(pk0 + packs));
-                ahead = true;
-            };
-            for (int j = first_stage(pk0); j < 2 * packs; j += 4) {
-                const uint32_t pk = pk0 + (j >> 1), p = pk % P_SLOTS;
-                ok = wait_parity(smem_u32(&bar->pk_full[p]), (pk / P_SLOTS) & 1, ctl, SITE_DEQUANT);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                // 128-byte swizzle: chunk c of row r lies at c ^ (r mod 8).
-                const uint32_t pr = sP + p * P_BYTES + trow * 128;
-                uint4 v[4];
+        uint32_t p = d, pp = 0, ep = 1;     // slot and parities of this group's next pack
+        bool ok = true, have = true;
+        auto tile_from = [&](int t, int b) {   // sets up tile t and requests its pack b
+            have = get_tile<BN, BR, BR>(a, off, tiles, t, w);
+            if (!have) return;
+            const size_t wr = min((size_t)weight_row(w, trow >> 4) + (trow & 15), (size_t)a.E * a.N - 1);
+            zrow = a.qzeros + wr * zwords;
+            rows = w.rows;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) v[c] = lds128(pr + (((4 * (j & 1) + c) ^ (trow & 7)) << 4));
-                const uint32_t it = 2 * pk0 + j, as = it % STAGES;
-                ok = wait_parity(smem_u32(&bar->empty[as]), ((it / STAGES) & 1) ^ 1, ctl, SITE_DEQUANT);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                if (j >= nst) {   // the depth ends inside the pack: an empty stage
-                    if (lane == 0) {
-                        mbar_arrive(smem_u32(&bar->pk_empty[p]));
-                        mbar_arrive(smem_u32(&bar->full[as]));
-                    }
-                    continue;
-                }
-                tc_fence_after();
-                const uint32_t xd = sX + as * X_BYTES + (c16 >> 3) * X_ATOM + rr * 128 + (((c16 ^ rr) & 7) << 4);
-                sts128(xd, permute_x(nx0));
-                sts128(xd + 8 * 128, permute_x(nx1));
-                fence_proxy_async_smem();
-                const int k0 = (dep.s0 + j) * SK;
-                const uint32_t cz = nz;
-                if (j + 4 < nst) {
-                    load_x(j + 4);
-                    if (word_of(j + 4) != nw) {
-                        nw = word_of(j + 4);
-                        nz = __ldg(zrow + nw);
-                    }
-                } else {
-                    next_tile();
-                }
-                const int g0 = k0 >> lg;
-                Zero<BF> z((cz >> (4 * (g0 & 7))) & 0xFu);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {   // 32 codes, all in one group
-                    if (c > 0 && a.gs < SK) {
-                        const int g = min((k0 + 32 * c) >> lg, groups - 1);
-                        z = Zero<BF>((cz >> (4 * (g & 7))) & 0xFu);
-                    }
-                    uint32_t o[16];
-                    code_word<BF>(v[c].x, magic, z, o);
-                    code_word<BF>(v[c].y, magic, z, o + 4);
-                    code_word<BF>(v[c].z, magic, z, o + 8);
-                    code_word<BF>(v[c].w, magic, z, o + 12);
-                    tmem_st_32x32b_x16(t_a + as * A_COLS + c * 16, o);
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&bar->pk_empty[p]));
-                    mbar_arrive(smem_u32(&bar->full[as]));
-                }
+            for (int i = 0; i < 4; ++i) {
+                if (q + 4 * i >= rows) continue;
+                int v = w.r0 + q + 4 * i;
+                if (a.rows) v = __ldg(a.rows + v);
+                // An index outside x reads row 0 (zeros are stored for it).
+                xp[i] = a.x + ((unsigned)v < (unsigned)a.T ? (size_t)v : 0) * pitch;
             }
-            if (ok && !ahead) next_tile();
+            if (b < packs) load(b);
+        };
+        tile_from(first, d);
+        for (int t = first; ok && have; t += stride, pk0 += packs) {
+            const int b0 = (int)((d - pk0) & 1);
+            if (b0 >= packs) {              // a tile of one pack, of the other group
+                tile_from(t + stride, (int)((d - pk0 - packs) & 1));
+                continue;
+            }
+            for (int b = b0; b < packs; b += 2) {
+                const int here = rows;
+                const uint32_t cz = nz;
+                ok = wait_parity2(smem_u32(&bar->pk_full[p]), pp, eb, ep, ctl, SITE_DEQUANT);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+                const uint32_t src = sP + p * P_BYTES + trow * 128;
+                const int k0 = (dep.s0 + 2 * b) * SK;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bool real = 2 * b + h < nst;   // the second stage of a tile's last pack may be empty
+                    if (real) {
+                        // 128-byte swizzle: chunk c of row r lies at c ^ (r mod 8).
+                        uint4 v[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) v[c] = lds128(src + (((4 * h + c) << 4) ^ r7));
+                        Zero<BF> z((cz >> (4 * (((k0 + h * SK) >> lg) & 7))) & 0xFu);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {    // 32 codes, all in one group
+                            if (c > 0 && a.gs < SK) z = Zero<BF>((cz >> (4 * (((k0 + h * SK + 32 * c) >> lg) & 7))) & 0xFu);
+                            uint32_t o[16];
+                            code_word<BF>(v[c].x, magic, z, o);
+                            code_word<BF>(v[c].y, magic, z, o + 4);
+                            code_word<BF>(v[c].z, magic, z, o + 8);
+                            code_word<BF>(v[c].w, magic, z, o + 12);
+                            tmem_st_32x32b_x16(t_a + h * A_COLS + c * 16, o);
+                        }
+                    }
+                    if (h == 0) {
+                        ok = wait_parity(eb + 8, ep, ctl, SITE_DEQUANT);
+                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = q + 4 * i;
+                            if (r < here) sts128(xd + r * 128 + (((lane ^ r) & 7) << 4), permute_x(nx[i]));
+                        }
+                        fence_proxy_async_smem();
+                        if (b + 2 < packs) load(b + 2);
+                        else tile_from(t + stride, (int)((d - pk0 - packs) & 1));
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (h == 1) mbar_arrive(smem_u32(&bar->pk_empty[p]));
+                        mbar_arrive(fb + 8 * h);
+                    }
+                }
+                if (!ok) break;
+                p += 2;
+                if (p >= P_SLOTS) {
+                    p -= P_SLOTS;
+                    pp ^= 1;
+                }
+                ep ^= 1;
+            }
         }
     }
 
