@@ -129,6 +129,29 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 // rounding that follows.
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
+// Clusters of `size` CTAs of a kernel that are resident at once (one CTA per SM; some GPCs have SMs left over), at
+// least 1.  A persistent grid of more clusters would run the rest after the others have finished.
+template <typename Kernel>
+int resident_clusters(Kernel kern, int threads, size_t smem, int size) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms() / size * size);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = num_sms() / size;
+    }
+    return n < 1 ? 1 : n;
+}
+
 // Map of the stacked weights for tiles of 128 rows x 128 bytes with the 128-byte swizzle (row_bytes: bytes of
 // a weight row).  SwiGLU with I % 16 == 0: the 5-D view [E][I / 16][2][16][row] (a.box), whose box of
 // 4 x 2 x 16 rows is 16 gate rows, their 16 up rows, and so on; otherwise boxes of 16 rows.

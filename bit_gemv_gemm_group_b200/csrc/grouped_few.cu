@@ -516,15 +516,17 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // CTAs of a cluster that share a tile's depth: the number (1, 2 or 4) with the shortest schedule, where a
-// round of tiles lasts its depth and a fixed part for the parts' exchange.
-int choose_split(long long tiles, int K, int sms) {
+// round of tiles lasts its depth and, for the parts' exchange, as long as two packs (64 experts, N = 4096,
+// K = 2048: 103 us unsplit, 144 us on pairs; 2 x 4096 x 14336: 31 us on pairs, 33 us on fours).
+int choose_split(long long tiles, int K, const int (&clusters)[3]) {
     const int packs = ((K + SK - 1) / SK + 1) / 2;
     int best = 1;
     double best_t = 1e300;
-    for (int s = 1; s <= MAX_SPLIT; s *= 2) {
+    for (int i = 0; i < 3; ++i) {
+        const int s = 1 << i;
         if (s > 1 && packs < 2 * s) break;
-        const long long clusters = sms / s, rounds = (tiles + clusters - 1) / clusters;
-        const double t = (double)rounds * ((double)packs / s + (s > 1 ? 1.0 : 0.0));
+        const long long rounds = (tiles + clusters[i] - 1) / clusters[i];
+        const double t = (double)rounds * ((double)packs / s + (s > 1 ? 2.0 : 0.0));
         if (t < 0.98 * best_t) {
             best_t = t;
             best = s;
@@ -536,13 +538,16 @@ int choose_split(long long tiles, int K, int sms) {
 template <bool BF, bool SWIGLU>
 wq_status launch(const CUtensorMap &tw, const Args &a, long long tiles, cudaStream_t st, const char *who) {
     auto kern = few_rows_kernel<BF, SWIGLU>;
-    const int split = choose_split(tiles, a.K, num_sms());
-    const size_t smem = smem_bytes(split, a.E);
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(MAX_SPLIT, MAX_E));
     if (e != cudaSuccess) return fail(WQ_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", who, cudaGetErrorString(e));
+    // Looked up once: every device of the library's kind answers the same.
+    static const int clusters[3] = {num_sms(), resident_clusters(kern, THREADS, smem_bytes(2, MAX_E), 2),
+                                    resident_clusters(kern, THREADS, smem_bytes(4, MAX_E), 4)};
+    const int split = choose_split(tiles, a.K, clusters);
+    const size_t smem = smem_bytes(split, a.E);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<long long>(num_sms() / split, tiles) * split);
+    cfg.gridDim = dim3((unsigned)std::min<long long>(clusters[split / 2], tiles) * split);
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
