@@ -152,10 +152,10 @@ int resident_clusters(Kernel kern, int threads, size_t smem, int size) {
     return n < 1 ? 1 : n;
 }
 
-// Map of the stacked weights for tiles of 128 rows x 128 bytes with the 128-byte swizzle (row_bytes: bytes of
-// a weight row).  SwiGLU with I % 16 == 0: the 5-D view [E][I / 16][2][16][row] (a.box), whose box of
+// Map of the stacked weights for tiles of 128 rows x `width` bytes, 64 or 128, with the swizzle of that width
+// (row_bytes: bytes of a weight row).  SwiGLU with I % 16 == 0: the 5-D view [E][I / 16][2][16][row] (a.box), whose box of
 // 4 x 2 x 16 rows is 16 gate rows, their 16 up rows, and so on; otherwise boxes of 16 rows.
-bool encode_weights(CUtensorMap *map, const void *w, uint64_t row_bytes, Args &a, bool swiglu);
+bool encode_weights(CUtensorMap *map, const void *w, uint64_t row_bytes, int width, Args &a, bool swiglu);
 
 // INT4 weights and at most a few dozen rows per expert (grouped_few.cu); `bf16`: type of x and y.
 wq_status few_rows_w4(const void *w, Args a, bool bf16, bool swiglu, cudaStream_t st, const char *who);

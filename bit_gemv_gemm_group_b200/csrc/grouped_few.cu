@@ -572,7 +572,7 @@ wq_status few_rows_w4(const void *w, Args a, bool bf16, bool swiglu, cudaStream_
     const long long most = ((long long)std::min(a.E, a.R) + a.R / BR) * a.nb;  // tiles of any offsets
     WQ_REQUIRE(most < INT_MAX / 2, WQ_ERR_UNSUPPORTED, "%s: R (%d) x N (%d) gives too many tiles", who, a.R, a.N);
     CUtensorMap tw;
-    if (!encode_weights(&tw, w, (uint64_t)a.K / 2, a, swiglu)) return WQ_ERR_CUDA;
+    if (!encode_weights(&tw, w, (uint64_t)a.K / 2, 128, a, swiglu)) return WQ_ERR_CUDA;
     if (bf16) return swiglu ? launch<true, true>(tw, a, most, st, who) : launch<true, false>(tw, a, most, st, who);
     return swiglu ? launch<false, true>(tw, a, most, st, who) : launch<false, false>(tw, a, most, st, who);
 }

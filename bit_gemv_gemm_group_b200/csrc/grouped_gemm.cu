@@ -24,12 +24,11 @@
 //   warp 1      an elected thread issues tcgen05.mma into one of two accumulators; in the pair's second CTA it
 //               passes on to the first that a stage is filled
 //   warp 2      allocates tensor memory
-//   warp 3      (INT4) packed weight tiles, 128 rows x 128 bytes (four stages), into a ring of their own:
-//               with 32-byte rows a TMA request took about 1000 cycles for its 4 KB
+//   warp 3      (INT4) packed weight tiles, 128 rows x 64 bytes (two stages), into a ring of their own
 //   warps 4-7   epilogue of the previous tile: scales, SwiGLU, conversion, stores (4-11 for 8-bit pairs)
 //   then        four warps that gather indexed activation rows by cp.async (TMA's gather of four rows a
 //               request took 32 cycles for its 512 bytes, four times what the MMAs leave), and for INT4
-//               four groups of four warps that dequantize every fourth stage each
+//               three groups of four warps that dequantize every third packed tile each
 #include "grouped.cuh"
 
 #include <algorithm>
@@ -45,10 +44,11 @@ enum Kind { K_I8, K_FP8, K_W4H, K_W4B };  // INT8, E4M3, INT4 weights with fp16 
 
 constexpr int STAGE_K = 128;           // bytes of k per stage and row (128 INT8/FP8 or 64 16-bit values)
 constexpr uint32_t A_BYTES = BM * STAGE_K;
-constexpr int PK = 4;                  // stages per packed INT4 tile (128 bytes of a weight row)
-constexpr uint32_t P_BYTES = BM * PK * 32;
-constexpr int EPI_WARP0 = 4, GATHER_WARPS = 4, DQ_GROUPS = 4;
-constexpr int MAX_STAGES = 8, MAX_PSTAGES = 3;
+constexpr int PK = 2;                  // stages per packed INT4 tile
+constexpr int P_ROW = PK * 32;         // and bytes of a weight row (128 codes)
+constexpr uint32_t P_BYTES = BM * P_ROW;
+constexpr int EPI_WARP0 = 4, GATHER_WARPS = 4, DQ_GROUPS = 3;
+constexpr int MAX_STAGES = 8, PSTAGES = DQ_GROUPS;   // packed slots: one per dequantizing group
 constexpr unsigned SITE_PRODUCER = 0x1001, SITE_MMA = 0x1002, SITE_EPILOGUE = 0x1004, SITE_DRAIN = 0x1008,
                    SITE_DEQUANT = 0x1010, SITE_PACKED = 0x1020, SITE_GATHER = 0x1040;
 
@@ -57,7 +57,7 @@ struct Bars {
     uint64_t put[MAX_STAGES];  // what warps write of a stage: gathered rows (an arrival per thread, when its
                                // copies land), dequantized weights (one per warp) and, in a pair's first CTA,
                                // word that the second's share is there
-    uint64_t pk_full[MAX_PSTAGES], pk_empty[MAX_PSTAGES];
+    uint64_t pk_full[PSTAGES], pk_empty[PSTAGES];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
     uint32_t tmem_base;
@@ -72,8 +72,7 @@ struct Layout {
     static constexpr int BR = PAIR ? 256 : 64;               // activation rows of a tile, at most
     static constexpr int SR = PAIR ? BR / 2 : BR;            // of them in this CTA's shared memory
     static constexpr uint32_t B_BYTES = SR * STAGE_K;
-    static constexpr int STAGES = PAIR ? (W4 ? 5 : 6) : 8;
-    static constexpr int PSTAGES = 3;                        // packed INT4 tiles
+    static constexpr int STAGES = PAIR ? 6 : 8;
     static constexpr int BOX = PAIR ? 64 : 16;               // rows per box when the activations lie in order
     static constexpr int EPI_WARPS = PAIR && !W4 ? 8 : 4;    // 8: two per 32 TMEM lanes, half the rows each
     static constexpr int GA_WARP0 = EPI_WARP0 + EPI_WARPS;
@@ -88,7 +87,7 @@ struct Layout {
     static constexpr size_t smem(int E) { return 1024 + OFF_TAB + 2 * (size_t)(E + 1) * 4; }
     static_assert(PAIR || !W4, "INT4 with few rows has a kernel of its own");
     static_assert(smem(MAX_E) <= 232448, "fits the shared memory of a CTA");
-    static_assert(STAGES <= MAX_STAGES && PSTAGES <= MAX_PSTAGES, "barrier arrays");
+    static_assert(STAGES <= MAX_STAGES && (!W4 || STAGES == PK * DQ_GROUPS), "ring: two stage slots per group");
 };
 static_assert(sizeof(Bars) <= 1024, "barriers fit their space");
 
@@ -176,7 +175,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                         const Args a) {
     using L = Layout<KIND, GATHER, PAIR>;
     constexpr bool W4 = L::W4, TMA_STAGE = !W4 || !GATHER;  // the stage's barrier `full` is used
-    constexpr int BR = L::BR, STEP = PAIR ? 32 : 16, STAGES = L::STAGES, PSTAGES = L::PSTAGES;
+    constexpr int BR = L::BR, STEP = PAIR ? 32 : 16, STAGES = L::STAGES;
     constexpr int BNC = SWIGLU ? BM / 2 : BM;          // output columns of this CTA's share of a tile
     constexpr int BN = PAIR ? 2 * BNC : BNC;
     constexpr int KE = W4 ? STAGE_K / 2 : STAGE_K;     // k values per stage
@@ -191,7 +190,8 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = PAIR ? (int)cluster_ctarank() : 0;
     const int first = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x, stride = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
-    const int kst = (a.K + KE - 1) / KE, packs = (kst + PK - 1) / PK;
+    // Stages of a tile.  INT4: whole packed tiles; past the depth codes and activations are zeros.
+    const int packs = (a.K + PK * KE - 1) / (PK * KE), kst = W4 ? packs * PK : (a.K + KE - 1) / KE;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
         }
         for (int p = 0; p < PSTAGES; ++p) {
             mbar_init(smem_u32(&bar->pk_full[p]), 1);
-            mbar_init(smem_u32(&bar->pk_empty[p]), 4 * DQ_GROUPS);
+            mbar_init(smem_u32(&bar->pk_empty[p]), 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bar->acc_full[i]), 1);
@@ -237,15 +237,16 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
     auto weight_row = [&](const Tile &t, int i) {
         return t.e * a.N + t.n0 + rank * BNC + (SWIGLU ? (i & 1) * (a.N / 2) + (i >> 1) * 16 : i * 16);
     };
-    // 128 bytes of k (block kb) of this CTA's 128 weight rows of tile w.  SwiGLU with I % 16 == 0: one box of
+    constexpr int WB = W4 ? P_ROW : STAGE_K;
+    // WB bytes of k (block kb) of this CTA's 128 weight rows of tile w.  SwiGLU with I % 16 == 0: one box of
     // the weights seen as [E][I / 16][2][16][K], whose rows come as 16 gate rows, their 16 up rows, ...
     auto load_weights = [&](uint32_t dst, uint32_t fb, int kb) {
         if (!SWIGLU) {
-            tma_load_2d(dst, &tmap_w, fb, kb * STAGE_K, weight_row(w, 0));
+            tma_load_2d(dst, &tmap_w, fb, kb * WB, weight_row(w, 0));
         } else if (a.box) {
-            tma_load_5d(dst, &tmap_w, fb, kb * STAGE_K, 0, 0, (w.n0 + rank * BNC) >> 4, w.e);
+            tma_load_5d(dst, &tmap_w, fb, kb * WB, 0, 0, (w.n0 + rank * BNC) >> 4, w.e);
         } else {
-            for (int i = 0; i < 8; ++i) tma_load_2d(dst + i * 16 * STAGE_K, &tmap_w, fb, kb * STAGE_K, weight_row(w, i));
+            for (int i = 0; i < 8; ++i) tma_load_2d(dst + i * 16 * WB, &tmap_w, fb, kb * WB, weight_row(w, i));
         }
     };
     // Activation rows that this CTA holds of tile t, and the first of them.
@@ -486,122 +487,93 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
         cp_async_wait_all();
     } else if (W4 && warp >= L::DQ_WARP0) {
         // -------------------------------------------------------------------- dequantizers
-        // Group g of four warps takes the g-th stage of every packed tile; a thread takes one weight row of it,
-        // 64 codes.
+        // Group d of four warps takes every third packed tile and fills stages 2 d and 2 d + 1 (packed and stage
+        // slots belong to one group each); a thread takes one weight row, 128 codes.
         constexpr bool BF = KIND == K_W4B;
         const uint32_t magic = opaque_const(BF ? 0x43004300u : 0x64006400u);
-        const int row = 32 * (warp & 3) + lane;
-        const uint32_t group = (uint32_t)(warp - L::DQ_WARP0) >> 2;
+        const int row = 32 * (warp & 3) + lane, d = (warp - L::DQ_WARP0) >> 2;
         const int lg = 31 - __clz(a.gs), groups = a.K >> lg, zwords = (groups + 7) / 8;
-        const bool vec = groups % 8 == 0;
+        const bool whole = a.K % (PK * KE) == 0;   // every packed tile is full, and its scales are aligned to their size
+        const uint32_t pf = smem_u32(&bar->pk_full[d]), pe = smem_u32(&bar->pk_empty[d]);
+        const uint32_t eb = smem_u32(&bar->empty[2 * d]), fb = smem_u32(&bar->put[2 * d]);
+        const uint32_t src = sP + d * P_BYTES + row * P_ROW, s3 = (uint32_t)((row >> 1) & 3) << 4;  // 64-byte swizzle
+        const uint32_t dst = sA + 2 * d * A_BYTES + row * STAGE_K, r7 = (uint32_t)(row & 7) << 4;   // 128-byte swizzle
         const uint16_t *srow = nullptr;
         const uint32_t *zrow = nullptr;
-        uint4 ns = {}, cs = {};   // scales and zeros of 8 groups: the next such window's and the current one's
-        uint32_t nz = 0, cz = 0;
-        auto rows_of = [&](const Tile &t) {
-            const size_t wr = min((size_t)weight_row(t, row >> 4) + (row & 15), (size_t)a.E * a.N - 1);
+        uint2 ns = {}, cs = {};   // scales (up to four) and zeros of the group's next packed tile and of this one
+        uint32_t nz = 0, cz = 0, pk0 = 0, ph = 0;
+        auto load = [&](int b) {
+            const int g = min(b * (PK * KE) >> lg, groups - 1);
+            nz = __ldg(zrow + (g >> 3));
+            const uint16_t *p = srow + g;
+            if (lg >= 7) {
+                ns.x = __ldg(p);
+            } else if (!whole) {
+                uint32_t v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = __ldg(srow + min(g + i, groups - 1));
+                ns = make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
+            } else if (lg == 6) {
+                ns.x = __ldg(reinterpret_cast<const uint32_t *>(p));
+            } else {
+                ns = __ldg(reinterpret_cast<const uint2 *>(p));
+            }
+        };
+        bool ok = true, have = true;
+        auto tile_from = [&](int t, int b) {   // sets up tile t and requests the scales of its packed tile b
+            have = get_tile<BN, BR, STEP>(a, off, tiles, t, w);
+            if (!have) return;
+            const size_t wr = min((size_t)weight_row(w, row >> 4) + (row & 15), (size_t)a.E * a.N - 1);
             srow = a.scales + wr * groups;
             zrow = a.qzeros + wr * zwords;
+            if (b < packs) load(b);
         };
-        auto load = [&](int b) {
-            nz = __ldg(zrow + b);
-            if (vec) {
-                ns = __ldg(reinterpret_cast<const uint4 *>(srow) + b);
-            } else {
-                uint32_t v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = __ldg(srow + min(8 * b + i, groups - 1));
-                ns = make_uint4(v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16));
+        auto first_of = [&](uint32_t pk) { return (int)((d + DQ_GROUPS - pk % DQ_GROUPS) % DQ_GROUPS); };
+        tile_from(first, d);
+        for (int t = first; ok && have; t += stride, pk0 += packs) {
+            int b = first_of(pk0);
+            if (b >= packs) {   // a short tile without a packed tile of this group's
+                tile_from(t + stride, first_of(pk0 + packs));
+                continue;
             }
-        };
-        uint32_t it0 = 0;         // stages before the tile
-        uint32_t p = 0, pp = 0;   // slot and phase parity of the packed tile
-        const uint32_t r7 = (uint32_t)(row & 7) << 4, in_row = sP + row * STAGE_K, out_row = sA + row * STAGE_K;
-        bool ok = true, have = get_tile<BN, BR, STEP>(a, off, tiles, first, w);
-        if (have) {
-            rows_of(w);
-            load(0);
-        }
-        for (int t = first; ok && have; t += stride, it0 += kst) {
-            // Window 0 of this tile has been loaded; the windows after it, and then the next tile's first,
-            // are requested when the one before them comes into use.
-            int win = 0;
-            cs = ns;
-            cz = nz;
-            bool ahead = false;   // ns, nz hold the next tile's window 0
-            auto request = [&](int b) {
-                if (b < zwords) {
-                    load(b);
-                } else {
-                    have = get_tile<BN, BR, STEP>(a, off, tiles, t + stride, w);
-                    if (have) {
-                        rows_of(w);
-                        load(0);
-                    }
-                    ahead = true;
-                }
-            };
-            request(1);
-            uint32_t st = (it0 + group) % STAGES, sp = ((it0 + group) / STAGES) & 1;   // this group's stage slot
-            for (int kb = (int)group; kb < packs * PK; kb += PK) {
-                const uint32_t pf = smem_u32(&bar->pk_full[p]), pe = smem_u32(&bar->pk_empty[p]);
-                if (kb >= kst) {  // the tile's depth ends inside the packed tile
-                    ok = wait_parity(pf, pp, ctl, SITE_DEQUANT);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    if (lane == 0) mbar_arrive(pe);
-                    if (++p == PSTAGES) {
-                        p = 0;
-                        pp ^= 1;
-                    }
-                    continue;
-                }
-                ok = wait_parity2(pf, pp, smem_u32(&bar->empty[st]), sp ^ 1, ctl, SITE_DEQUANT);
+            for (; b < packs; b += DQ_GROUPS, ph ^= 1) {
+                cs = ns;
+                cz = nz;
+                const int k0 = b * (PK * KE);
+                ok = wait_parity2(pf, ph, eb, ph ^ 1, ctl, SITE_DEQUANT);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                // 128-byte swizzle: chunk c of row r lies at c ^ (r mod 8).
-                const uint32_t src = in_row + p * P_BYTES, dst = out_row + st * A_BYTES;
-                const uint4 q0 = lds128(src + ((2 * group << 4) ^ r7)), q1 = lds128(src + (((2 * group + 1) << 4) ^ r7));
-                const int g0 = min((kb * KE) >> lg, groups - 1), g1 = min((kb * KE + 32) >> lg, groups - 1);
-                if ((g0 >> 3) != win) {
-                    win = g0 >> 3;
-                    cs = ns;
-                    cz = nz;
-                    request(win + 1);
-                }
-                auto constants = [&](int g) {
-                    const int i = g & 7;
-                    const uint32_t pr = i < 4 ? (i < 2 ? cs.x : cs.y) : (i < 6 ? cs.z : cs.w);
-                    GroupConst<BF> c;
-                    c.set((i & 1) ? pr >> 16 : pr & 0xFFFFu, (cz >> (4 * i)) & 0xFu);
-                    return c;
-                };
-                GroupConst<BF> c = constants(g0);
-                const uint32_t w0[4] = {q0.x, q0.y, q0.z, q0.w}, w1[4] = {q1.x, q1.y, q1.z, q1.w};
+                uint4 v[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sts128(dst + ((j << 4) ^ r7), dequant_word<BF>(w0[j], magic, c));
-                if (g1 != g0) c = constants(g1);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sts128(dst + (((4 + j) << 4) ^ r7), dequant_word<BF>(w1[j], magic, c));
+                for (int c = 0; c < 4; ++c) v[c] = lds128(src + ((c << 4) ^ s3));
+                // The codes are in registers: the slot goes back (the fence orders the reads before the next copy).
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(pe);
-                    mbar_arrive(smem_u32(&bar->put[st]));
+                if (lane == 0) mbar_arrive(pe);
+                if (b + DQ_GROUPS < packs) load(b + DQ_GROUPS);
+                else tile_from(t + stride, first_of(pk0 + packs));
+                GroupConst<BF> gc;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {   // 32 codes, all in one group; two of these make a stage
+                    if (h == 0 || (h << 5 & (a.gs - 1)) == 0) {
+                        const int g = min((k0 + 32 * h) >> lg, groups - 1), i = g - min(k0 >> lg, groups - 1);
+                        const uint32_t s2 = i < 2 ? cs.x : cs.y;
+                        gc.set((i & 1) ? s2 >> 16 : s2 & 0xFFFFu, (cz >> (4 * (g & 7))) & 0xFu);
+                    }
+                    if (h == 2) {
+                        ok = wait_parity(eb + 8, ph ^ 1, ctl, SITE_DEQUANT);
+                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    }
+                    const uint32_t words[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        sts128(dst + (h >> 1) * A_BYTES + (((4 * (h & 1) + j) << 4) ^ r7), dequant_word<BF>(words[j], magic, gc));
+                    if (h & 1) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(fb + 8 * (h >> 1));
+                    }
                 }
-                if (++p == PSTAGES) {
-                    p = 0;
-                    pp ^= 1;
-                }
-                // Four stages on: the slot before this one, of the next round of the ring unless this is slot 0.
-                static_assert(!W4 || STAGES == PK + 1, "ring step");
-                sp ^= st > 0;
-                st = st > 0 ? st - 1 : STAGES - 1;
-            }
-            if (ok && !ahead) {
-                have = get_tile<BN, BR, STEP>(a, off, tiles, t + stride, w);
-                if (have) {
-                    rows_of(w);
-                    load(0);
-                }
+                if (!ok) break;
             }
         }
     }
@@ -660,6 +632,7 @@ wq_status dispatch(const void *w, Args a, bool swiglu, cudaStream_t st, const ch
     const long long most = ((long long)std::min(a.E, a.R) + a.R / br) * a.nb;  // tiles of any offsets
     WQ_REQUIRE(most < INT_MAX / 2, WQ_ERR_UNSUPPORTED, "%s: R (%d) x N (%d) gives too many tiles", who, a.R, a.N);
     const bool gather = a.rows != nullptr;
+    constexpr int W_BYTES = W4 ? P_ROW : STAGE_K;   // of a weight row per copy
     CUtensorMap tx, tw;
     const CUtensorMapDataType xt = KIND == K_W4H ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                  : KIND == K_W4B ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -668,7 +641,7 @@ wq_status dispatch(const void *w, Args a, bool swiglu, cudaStream_t st, const ch
                         Layout<KIND, false, PAIR>::BOX,
                         CU_TENSOR_MAP_SWIZZLE_128B))
         return WQ_ERR_CUDA;
-    if (!encode_weights(&tw, w, W4 ? (uint64_t)a.K / 2 : (uint64_t)a.K, a, swiglu)) return WQ_ERR_CUDA;
+    if (!encode_weights(&tw, w, W4 ? (uint64_t)a.K / 2 : (uint64_t)a.K, W_BYTES, a, swiglu)) return WQ_ERR_CUDA;
     if (gather)
         return swiglu ? launch<KIND, true, true, PAIR>(tx, tw, a, most, st, who)
                       : launch<KIND, true, false, PAIR>(tx, tw, a, most, st, who);
@@ -689,16 +662,17 @@ wq_status run(const void *x, const void *w, Args a, bool swiglu, cudaStream_t st
 
 }  // namespace
 
-bool grouped::encode_weights(CUtensorMap *map, const void *w, uint64_t row_bytes, Args &a, bool swiglu) {
+bool grouped::encode_weights(CUtensorMap *map, const void *w, uint64_t row_bytes, int width, Args &a, bool swiglu) {
     const uint64_t half = (uint64_t)a.N / 2;
+    const CUtensorMapSwizzle swizzle = width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     a.box = swiglu && half % 16 == 0;
     if (!a.box)
-        return encode_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, row_bytes, (uint64_t)a.E * a.N, row_bytes, 128,
-                              swiglu ? 16 : BM, CU_TENSOR_MAP_SWIZZLE_128B);
+        return encode_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, row_bytes, (uint64_t)a.E * a.N, row_bytes, width,
+                              swiglu ? 16 : BM, swizzle);
     const uint64_t dims[5] = {row_bytes, 16, 2, half / 16, (uint64_t)a.E};
     const uint64_t strides[4] = {row_bytes, half * row_bytes, 16 * row_bytes, (uint64_t)a.N * row_bytes};
-    const uint32_t box[5] = {128, 16, 2, 4, 1};
-    return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, w, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    const uint32_t box[5] = {(uint32_t)width, 16, 2, 4, 1};
+    return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, w, dims, strides, box, swizzle);
 }
 
 namespace {

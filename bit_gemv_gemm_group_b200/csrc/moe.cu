@@ -7,13 +7,12 @@
 // of the T k (token, choice) pairs by expert, so that the rows of an expert are in token order and the
 // result never depends on the order in which blocks run.
 //
-// A warp takes one token: lane l holds logits l, l + 32, ... as order-preserving 32-bit keys, and each
-// of the k rounds is a lane-local maximum, one warp maximum of the keys and one warp minimum of the
-// indices that hold it.  A block of 32 warps takes chunks of 128 tokens.  Up to 128 tokens one block
-// does everything in one launch.  Above, the first launch writes ids, weights and each block's expert
-// counts, and the second adds up the counts of the blocks before its own, ranks its tokens and writes
-// rows and slots; ranks come from a bit per (expert, token) of the chunk, so no order-dependent atomic
-// decides a position.
+// A warp takes one token: lane l holds E / 32 neighbouring logits as order-preserving 32-bit keys, and each of
+// the k rounds is one warp maximum, a ballot whose lowest lane is the lowest expert that holds it, and a pop in
+// that lane.  Up to 64 tokens one block does everything in one launch.  Above, the first launch writes ids,
+// weights and each block's expert counts, and the second adds up the counts of the blocks before its own, ranks
+// its tokens and writes rows and slots; ranks come from a bit per (expert, token) of the chunk, so no
+// order-dependent atomic decides a position.
 #include "wq_device.cuh"
 #include "wq_host.h"
 
@@ -24,10 +23,11 @@ namespace wq {
 namespace {
 
 constexpr int CHUNK = 128;        // tokens ranked at a time: four 32-bit words per expert
-constexpr int ROUTE_WARPS = 32;
-constexpr int ROUTE_THREADS = 32 * ROUTE_WARPS;
-constexpr int MAX_BLOCKS = 256;   // the second launch reads every block's counts: few, larger blocks
-constexpr int MAX_E = 512, MAX_K = 32;
+constexpr int ONE_T = 64;         // tokens of a single block (128: 14.7 us; two launches 12.5 us)
+constexpr int ONE_THREADS = 1024; // the single block of up to ONE_T tokens
+constexpr int THREADS = 512;      // blocks of larger batches
+constexpr int MIN_PER_BLOCK = 16, MAX_BLOCKS = 256;  // the second launch reads every block's counts
+constexpr int MAX_E = 512, MAX_K = 32, MAX_T = MAX_BLOCKS * 32768;  // counts are 16 bits wide
 constexpr uint32_t KEY_NONE = 0x007FFFFFu;  // key of -inf; keys at or below it are not selectable
 
 __device__ __forceinline__ float load_logit(const float *p) { return __ldg(p); }
@@ -54,47 +54,90 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// Larger keys first; exchanges of neighbours leave equal ones in their order.
+__device__ __forceinline__ void order2(uint32_t &ka, int &ia, uint32_t &kb, int &ib) {
+    if (kb > ka) {
+        const uint32_t k = ka;
+        ka = kb;
+        kb = k;
+        const int i = ia;
+        ia = ib;
+        ib = i;
+    }
+}
+
 // One token's choice by one warp: lane j < k returns the j-th expert (-1 where none is left) and its weight.
 template <typename T, int EPL>
 __device__ __forceinline__ void choose(const T *__restrict__ row, int E, int k, bool renorm, int lane, int &id,
                                        float &weight) {
     uint32_t key[EPL];
+    int at[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        const int e = lane + 32 * i;
-        key[i] = e < E ? logit_key(load_logit(row + e)) : 0u;
+        at[i] = lane * EPL + i;
+        key[i] = at[i] < E ? logit_key(load_logit(row + at[i])) : 0u;
+    }
+    float all = 0.0f, top = 0.0f;
+    if (!renorm) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) best = max(best, key[i]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        if (best > KEY_NONE) {
+            top = key_logit(best);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (key[i] > KEY_NONE) all += exp_below(key_logit(key[i]), top);
+        }
+        all = warp_sum(all);
+    }
+    // Up to four keys a lane are sorted once, and a round pops the winner's first.  With more, the winner's
+    // largest is found again.
+    constexpr bool SORTED = EPL <= 4;
+    if (SORTED && EPL > 1) {
+#pragma unroll
+        for (int p = 0; p < EPL - 1; ++p)
+#pragma unroll
+            for (int i = 0; i + 1 < EPL - p; ++i) order2(key[i], at[i], key[i + 1], at[i + 1]);
     }
     id = -1;
-    float mine = 0.0f, top = 0.0f, all = 0.0f;
+    uint32_t mine_key = 0u;
     for (int j = 0; j < k; ++j) {
-        uint32_t best = 0u;
-        int at = 0;
+        uint32_t best = key[0];
+        int where = at[0];
+        if (!SORTED) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
-            }
+            for (int i = 1; i < EPL; ++i)
+                if (key[i] > best) {
+                    best = key[i];
+                    where = at[i];
+                }
+        }
         const uint32_t m = __reduce_max_sync(0xffffffffu, best);
         if (m <= KEY_NONE) break;
-        const unsigned e = __reduce_min_sync(0xffffffffu, best == m ? (unsigned)(lane + 32 * at) : UINT_MAX);
-        if (j == 0) {
-            top = key_logit(m);
-            if (!renorm) {
+        const int win = __ffs(__ballot_sync(0xffffffffu, best == m)) - 1;
+        const int e = __shfl_sync(0xffffffffu, where, win);
+        if (lane == j) {
+            id = e;
+            mine_key = m;
+        }
+        if (lane == win) {
+            if (SORTED) {
+#pragma unroll
+                for (int i = 0; i + 1 < EPL; ++i) {
+                    key[i] = key[i + 1];
+                    at[i] = at[i + 1];
+                }
+                key[EPL - 1] = 0u;
+            } else {
 #pragma unroll
                 for (int i = 0; i < EPL; ++i)
-                    if (key[i] > KEY_NONE) all += exp_below(key_logit(key[i]), top);
-                all = warp_sum(all);
+                    if (at[i] == where) key[i] = 0u;
             }
         }
-        if (lane == j) {
-            id = (int)e;
-            mine = exp_below(key_logit(m), top);
-        }
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (e == (unsigned)(lane + 32 * i)) key[i] = 0u;
     }
+    const uint32_t top_key = __shfl_sync(0xffffffffu, mine_key, 0);
+    const float mine = id >= 0 ? exp_below(key_logit(mine_key), key_logit(top_key)) : 0.0f;
     if (renorm) all = warp_sum(mine);
     weight = id >= 0 ? __fdiv_rn(mine, all) : 0.0f;
 }
@@ -117,25 +160,28 @@ __device__ __forceinline__ void scan_counts(const int *cnt, int *base, int E, in
 }
 
 struct RouteArgs {
-    int T, E, k, per_block;  // per_block: tokens of one block, a multiple of CHUNK
+    int T, E, k, per_block;  // per_block: tokens of one block
     int32_t *ids;
     float *weights;
     int32_t *offsets, *rows, *slots;
-    int *counts;             // [blocks][E]
+    uint16_t *counts;        // [blocks][E rounded up to 8]
 };
 
+__host__ __device__ constexpr int pitch_of(int E) { return (E + 7) & ~7; }
+
 // Positions of one chunk's pairs: bits[e][w] has bit t % 32 of word t / 32 set when token t of the
-// chunk chose e; a pair's rank is the number of set bits below its own, after base[e].
-__device__ __forceinline__ void mark(uint32_t *bits, const RouteArgs &a, int t0, int n) {
-    for (int i = threadIdx.x; i < n * a.k; i += blockDim.x) {
-        const int t = i / a.k, e = a.ids[(size_t)t0 * a.k + i];
+// chunk chose e; a pair's rank is the number of set bits below its own, after base[e].  `ids`: the chunk's.
+__device__ __forceinline__ void mark(uint32_t *bits, const int32_t *ids, int pairs, int k) {
+    for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
+        const int t = i / k, e = ids[i];
         if (e >= 0) atomicOr(&bits[4 * e + (t >> 5)], 1u << (t & 31));
     }
 }
 
-__device__ __forceinline__ void place(const uint32_t *bits, const int *base, const RouteArgs &a, int t0, int n) {
-    for (int i = threadIdx.x; i < n * a.k; i += blockDim.x) {
-        const int t = i / a.k, e = a.ids[(size_t)t0 * a.k + i];
+__device__ __forceinline__ void place(const uint32_t *bits, const int *base, const int32_t *ids, const RouteArgs &a,
+                                      int t0, int pairs) {
+    for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
+        const int t = i / a.k, e = ids[i];
         int p = -1;
         if (e >= 0) {
             p = base[e] + __popc(bits[4 * e + (t >> 5)] & ((1u << (t & 31)) - 1u));
@@ -152,106 +198,132 @@ __device__ __forceinline__ int set_bits(const uint32_t *bits, int e) {
 
 // Choices of the block's tokens; ONE: the whole of T is this block's single chunk, ranked at once.
 template <typename T, int EPL, bool ONE>
-__global__ void __launch_bounds__(ROUTE_THREADS) route_choose_kernel(const T *__restrict__ logits, RouteArgs a,
-                                                                     bool renorm) {
-    extern __shared__ int sh[];  // ONE: bits [E][4], counts [E], base [E + 1]; else counts [E]
+__global__ void __launch_bounds__(ONE ? ONE_THREADS : THREADS) route_choose_kernel(const T *__restrict__ logits,
+                                                                                   RouteArgs a, bool renorm) {
+    extern __shared__ int sh[];  // ONE: bits [E][4], counts [E], base [E + 1], ids [T k]; else counts [E]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t0 = (int)blockIdx.x * a.per_block, t1 = min(a.T, t0 + a.per_block);
+    const int t0 = (int)blockIdx.x * a.per_block, t1 = ONE ? a.T : min(a.T, t0 + a.per_block);
     int *cnt = ONE ? sh + 4 * a.E : sh;
-    for (int i = threadIdx.x; i < (ONE ? 5 : 1) * a.E; i += ROUTE_THREADS) sh[i] = 0;
+    int32_t *ids = ONE ? sh + 6 * a.E + 1 : nullptr;
+    for (int i = threadIdx.x; i < (ONE ? 5 : 1) * a.E; i += blockDim.x) sh[i] = 0;
+    if (!ONE) asm volatile("griddepcontrol.launch_dependents;");  // route_place_kernel waits for this grid itself
     __syncthreads();
-    for (int t = t0 + warp; t < t1; t += ROUTE_WARPS) {
+    for (int t = t0 + warp; t < t1; t += (int)blockDim.x / 32) {
         int id;
         float w;
         choose<T, EPL>(logits + (size_t)t * a.E, a.E, a.k, renorm, lane, id, w);
         if (lane < a.k) {
             a.ids[(size_t)t * a.k + lane] = id;
             a.weights[(size_t)t * a.k + lane] = w;
+            if (ONE) ids[t * a.k + lane] = id;
             if (id >= 0) atomicAdd(&cnt[id], 1);
         }
     }
     __syncthreads();
     if (!ONE) {
-        for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS) a.counts[(size_t)blockIdx.x * a.E + e] = cnt[e];
+        const int pitch = pitch_of(a.E);
+        for (int e = threadIdx.x; e < pitch; e += blockDim.x)
+            a.counts[(size_t)blockIdx.x * pitch + e] = (uint16_t)(e < a.E ? cnt[e] : 0);
         return;
     }
     uint32_t *bits = reinterpret_cast<uint32_t *>(sh);
     int *base = cnt + a.E;
-    mark(bits, a, 0, a.T);
+    mark(bits, ids, a.T * a.k, a.k);
     if (warp == 0) scan_counts(cnt, base, a.E, lane);
     __syncthreads();
-    place(bits, base, a, 0, a.T);
-    for (int e = threadIdx.x; e <= a.E; e += ROUTE_THREADS) a.offsets[e] = base[e];
-    for (int p = base[a.E] + threadIdx.x; p < a.T * a.k; p += ROUTE_THREADS) a.rows[p] = -1;
+    place(bits, base, ids, a, 0, a.T * a.k);
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.offsets[e] = base[e];
+    for (int p = base[a.E] + threadIdx.x; p < a.T * a.k; p += blockDim.x) a.rows[p] = -1;
 }
 
-__global__ void __launch_bounds__(ROUTE_THREADS) route_place_kernel(RouteArgs a) {
-    extern __shared__ int sh[];  // bits [E][4], totals [E], before [E], base [E + 1]
-    const int E = a.E;
+__global__ void __launch_bounds__(THREADS) route_place_kernel(RouteArgs a) {
+    extern __shared__ int sh[];  // bits [E][4], totals [E8], before [E8], base [E + 1]
+    const int E = a.E, pitch = pitch_of(E);
     uint32_t *bits = reinterpret_cast<uint32_t *>(sh);
-    int *total = sh + 4 * E, *before = total + E, *base = before + E;
-    const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < 6 * E; i += ROUTE_THREADS) sh[i] = 0;
+    int *total = sh + 4 * E, *before = total + pitch, *base = before + pitch;
+    for (int i = threadIdx.x; i < 4 * E + 2 * pitch; i += THREADS) sh[i] = 0;
     __syncthreads();
-    // Every thread adds one expert's counts over every (ROUTE_THREADS / E)-th block: sums of integers,
-    // the same in any order.
-    const int parts = max(1, ROUTE_THREADS / E), part = threadIdx.x / E, e0 = threadIdx.x % E;
+    // Launched before route_choose_kernel is done: nothing above reads what that writes.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // A thread adds eight experts' counts over every parts-th block: sums of integers, the same in any order.
+    const int cols = pitch / 8, parts = THREADS / cols, part = threadIdx.x / cols, e0 = 8 * (threadIdx.x % cols);
     if (part < parts) {
-        int all = 0, low = 0;
-#pragma unroll 4
+        int all[8] = {}, low[8] = {};
+#pragma unroll 8
         for (int b = part; b < (int)gridDim.x; b += parts) {
-            const int v = a.counts[(size_t)b * E + e0];
-            all += v;
-            low += b < (int)blockIdx.x ? v : 0;
+            const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(a.counts + (size_t)b * pitch + e0));
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            const bool is_low = b < (int)blockIdx.x;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int n = (u[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
+                all[i] += n;
+                low[i] += is_low ? n : 0;
+            }
         }
-        if (all) atomicAdd(&total[e0], all);
-        if (low) atomicAdd(&before[e0], low);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (all[i]) atomicAdd(&total[e0 + i], all[i]);
+            if (low[i]) atomicAdd(&before[e0 + i], low[i]);
+        }
     }
     __syncthreads();
-    if (threadIdx.x < 32) scan_counts(total, base, E, lane);
+    if (threadIdx.x < 32) scan_counts(total, base, E, threadIdx.x);
     __syncthreads();
-    const int last = base[E];
     if (blockIdx.x == 0)
-        for (int e = threadIdx.x; e <= E; e += ROUTE_THREADS) a.offsets[e] = base[e];
-    for (long long p = last + (long long)blockIdx.x * ROUTE_THREADS + threadIdx.x; p < (long long)a.T * a.k;
-         p += (long long)gridDim.x * ROUTE_THREADS)
+        for (int e = threadIdx.x; e <= E; e += THREADS) a.offsets[e] = base[e];
+    for (long long p = base[E] + (long long)blockIdx.x * THREADS + threadIdx.x; p < (long long)a.T * a.k;
+         p += (long long)gridDim.x * THREADS)
         a.rows[p] = -1;
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += ROUTE_THREADS) base[e] += before[e];
+    for (int e = threadIdx.x; e < E; e += THREADS) base[e] += before[e];
     const int t0 = (int)blockIdx.x * a.per_block, t1 = min(a.T, t0 + a.per_block);
     for (int t = t0; t < t1; t += CHUNK) {
-        const int n = min(CHUNK, t1 - t);
+        const int pairs = min(CHUNK, t1 - t) * a.k;
+        const int32_t *ids = a.ids + (size_t)t * a.k;
         __syncthreads();
-        mark(bits, a, t, n);
+        mark(bits, ids, pairs, a.k);
         __syncthreads();
-        place(bits, base, a, t, n);
+        place(bits, base, ids, a, t, pairs);
         __syncthreads();
-        for (int e = threadIdx.x; e < E; e += ROUTE_THREADS) {
+        for (int e = threadIdx.x; e < E; e += THREADS) {
             base[e] += set_bits(bits, e);
             bits[4 * e] = bits[4 * e + 1] = bits[4 * e + 2] = bits[4 * e + 3] = 0u;
         }
     }
 }
 
-// Tokens per block: one chunk, doubled until MAX_BLOCKS blocks cover T.
+// Tokens per block: a token per warp, doubled until MAX_BLOCKS blocks cover T.
 int tokens_per_block(int T) {
-    long long per = CHUNK;
-    while (per * MAX_BLOCKS < T) per *= 2;
-    return (int)per;
+    int per = MIN_PER_BLOCK;
+    while ((long long)per * MAX_BLOCKS < T) per *= 2;
+    return per;
 }
 
 template <typename T, int EPL>
-wq_status route_launch(const T *logits, RouteArgs a, bool renorm, cudaStream_t st) {
-    if (a.T <= CHUNK) {
-        route_choose_kernel<T, EPL, true><<<1, ROUTE_THREADS, (6 * a.E + 1) * sizeof(int), st>>>(logits, a, renorm);
+wq_status route_launch(const T *logits, const RouteArgs &a, bool renorm, cudaStream_t st) {
+    if (a.T <= ONE_T) {
+        const size_t smem = (6 * a.E + 1 + a.T * a.k) * sizeof(int);
+        route_choose_kernel<T, EPL, true><<<1, ONE_THREADS, smem, st>>>(logits, a, renorm);
         return check_launch("wq_moe_route");
     }
     const int blocks = (a.T + a.per_block - 1) / a.per_block;
-    route_choose_kernel<T, EPL, false><<<blocks, ROUTE_THREADS, a.E * sizeof(int), st>>>(logits, a, renorm);
+    route_choose_kernel<T, EPL, false><<<blocks, THREADS, a.E * sizeof(int), st>>>(logits, a, renorm);
     const wq_status e = check_launch("wq_moe_route");
     if (e != WQ_OK) return e;
-    route_place_kernel<<<blocks, ROUTE_THREADS, (7 * a.E + 1) * sizeof(int), st>>>(a);
-    return check_launch("wq_moe_route");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = (5 * a.E + 1 + 2 * pitch_of(a.E)) * sizeof(int);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t le = cudaLaunchKernelEx(&cfg, route_place_kernel, a);
+    if (le != cudaSuccess) return fail(WQ_ERR_CUDA, "wq_moe_route: launch failed: %s", cudaGetErrorString(le));
+    return WQ_OK;
 }
 
 template <typename T>
@@ -356,9 +428,9 @@ wq_status combine_dispatch(const uint16_t *y, int R, const float *weights, const
 }  // namespace wq
 
 extern "C" size_t wq_moe_route_workspace_bytes(int T, int E) {
-    if (T <= wq::CHUNK || E <= 0) return 0;
+    if (T <= wq::ONE_T || T > wq::MAX_T || E <= 0) return 0;
     const int per = wq::tokens_per_block(T);
-    return (size_t)((T + per - 1) / per) * (size_t)E * sizeof(int);
+    return (size_t)((T + per - 1) / per) * (size_t)wq::pitch_of(E) * sizeof(uint16_t);
 }
 
 extern "C" wq_status wq_moe_route(const void *logits, wq_dtype dtype, int T, int E, int top_k, int renormalize,
@@ -378,10 +450,11 @@ extern "C" wq_status wq_moe_route(const void *logits, wq_dtype dtype, int T, int
     WQ_REQUIRE(top_k <= E, WQ_ERR_INVALID_ARG, "wq_moe_route: top_k (%d) must be at most E (%d)", top_k, E);
     WQ_REQUIRE(E <= MAX_E && top_k <= MAX_K, WQ_ERR_UNSUPPORTED,
                "wq_moe_route: E (%d) must be at most %d and top_k (%d) at most %d", E, MAX_E, top_k, MAX_K);
-    WQ_REQUIRE((long long)T * top_k <= INT_MAX, WQ_ERR_UNSUPPORTED, "wq_moe_route: T * top_k must be below 2^31");
+    WQ_REQUIRE(T <= MAX_T && (long long)T * top_k <= INT_MAX, WQ_ERR_UNSUPPORTED,
+               "wq_moe_route: T (%d) must be at most %d, and T * top_k below 2^31", T, MAX_T);
     if (wq_moe_route_workspace_bytes(T, E)) WQ_REQUIRE_PTR(workspace, "workspace");
     const RouteArgs a{T, E, top_k, tokens_per_block(T), ids, weights, offsets, rows, slots,
-                      static_cast<int *>(workspace)};
+                      static_cast<uint16_t *>(workspace)};
     cudaStream_t st = as_stream(stream);
     if (dtype == WQ_F32) return route_dispatch<float>(logits, a, renormalize != 0, st);
     if (dtype == WQ_F16) return route_dispatch<__half>(logits, a, renormalize != 0, st);

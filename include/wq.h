@@ -445,9 +445,9 @@ wq_status wq_awq(const uint16_t *w, int N, int K, int group_size, const uint16_t
  * logits: [T][E] of dtype WQ_F32, WQ_F16 or WQ_BF16;  ids: out int32
  * [T][top_k];  weights: out fp32 [T][top_k];  offsets: out int32 [E + 1];
  * rows: out int32 [T * top_k];  slots: out int32 [T][top_k].  workspace:
- * wq_moe_route_workspace_bytes(T, E) bytes (0, and NULL is taken, for T <= 128),
+ * wq_moe_route_workspace_bytes(T, E) bytes (0, and NULL is taken, for T <= 64),
  * 16-byte aligned, contents on entry do not matter; calls that share one must not overlap on the GPU.
- * 1 <= top_k <= min(E, 32), E <= 512, T * top_k < 2^31.
+ * 1 <= top_k <= min(E, 32), E <= 512, T <= 2^23, T * top_k < 2^31.
  */
 size_t wq_moe_route_workspace_bytes(int T, int E);
 wq_status wq_moe_route(const void *logits, wq_dtype dtype, int T, int E, int top_k, int renormalize, int32_t *ids,

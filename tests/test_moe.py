@@ -43,15 +43,17 @@ def test_route_refusals(wq):
     assert _route(wq, dtype=5) == inv
     assert _route(wq, k=9) == inv                      # top_k > E
     assert _route(wq, E=513) == una and _route(wq, E=64, k=33) == una
-    assert _route(wq, T=1 << 30, k=8) == una           # T * top_k
+    assert _route(wq, T=(1 << 23) + 1, k=1) == una and _route(wq, T=1 << 23, E=512, k=32, ws=None) == inv
     assert _route(wq, T=129, ws=None) == inv           # needs a workspace
 
 
 def test_route_workspace(wq):
-    assert wq.moe_route_workspace_bytes(128, 64) == 0 and wq.moe_route_workspace_bytes(0, 64) == 0
-    assert wq.moe_route_workspace_bytes(129, 64) == 2 * 64 * 4
-    assert wq.moe_route_workspace_bytes(128 * 256, 8) == 256 * 8 * 4
-    assert wq.moe_route_workspace_bytes(128 * 256 + 1, 8) == 129 * 8 * 4   # 256 tokens per block above that
+    assert wq.moe_route_workspace_bytes(64, 64) == 0 and wq.moe_route_workspace_bytes(0, 64) == 0
+    # 16-bit counts of every block (16 tokens each, doubled until 256 blocks cover T), experts padded to 8
+    assert wq.moe_route_workspace_bytes(129, 64) == 9 * 64 * 2
+    assert wq.moe_route_workspace_bytes(130, 9) == 9 * 16 * 2
+    assert wq.moe_route_workspace_bytes(16 * 256, 8) == 256 * 8 * 2
+    assert wq.moe_route_workspace_bytes(16 * 256 + 1, 8) == 129 * 8 * 2
 
 
 def _w4(wq, x=FAKE, T=4, rows=FAKE, off=FAKE, R=8, E=2, N=64, K=256, g=128, sw=0, y=FAKE, bf=False):
@@ -136,8 +138,9 @@ def check_route(got, logits, k, renorm):
 
 
 @gpu
-@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (3, 5, 5), (32, 64, 8), (128, 128, 8), (129, 128, 8),
-                                   (700, 33, 3), (1000, 512, 32), (257, 500, 7), (128 * 256 + 77, 16, 2)])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (3, 5, 5), (32, 64, 8), (64, 128, 8), (65, 128, 8), (128, 128, 8), (129, 128, 8),
+                                   (700, 33, 3), (1000, 512, 32), (257, 500, 7), (4096, 130, 4), (16 * 256 + 5, 64, 8),
+                                   (128 * 256 + 77, 16, 2), (200000, 24, 1)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
 def test_route(wq, T, E, k, dtype):
     g = torch.Generator().manual_seed(T * 1000 + E)
