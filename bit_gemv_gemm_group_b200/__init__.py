@@ -572,13 +572,12 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, worksp
             return moe_route(logits, top_k, renormalize, workspace)
     T, E = logits.shape
     k = int(top_k)
-    pairs = T * max(k, 0)
+    cols = max(k, 0)
     new = logits.new_empty
-    ids, slots = new((2, T, max(k, 0)), dtype=torch.int32).unbind(0) if pairs % 4 == 0 else \
-        (new((T, max(k, 0)), dtype=torch.int32), new((T, max(k, 0)), dtype=torch.int32))  # 16-byte aligned each
-    weights = new((T, max(k, 0)), dtype=torch.float32)
+    ids, slots = new((T, cols), dtype=torch.int32), new((T, cols), dtype=torch.int32)
+    weights = new((T, cols), dtype=torch.float32)
     offsets = new((E + 1,), dtype=torch.int32)
-    rows = new((pairs,), dtype=torch.int32)
+    rows = new((T * cols,), dtype=torch.int32)
     need = lib.wq_moe_route_workspace_bytes(T, E)
     if workspace is None:
         workspace = new((need,), dtype=torch.uint8) if need else None

@@ -677,6 +677,8 @@ bool grouped::encode_weights(CUtensorMap *map, const void *w, uint64_t row_bytes
 
 namespace {
 
+constexpr int MAX_SIZE = 1 << 29;   // row numbers and bytes of a row stay within 32 bits
+
 // Checks that every grouped product makes of its sizes.
 wq_status check_sizes(const char *who, int T, const int32_t *rows, const int32_t *offsets, int R, int E, int N, int K,
                       int swiglu) {
@@ -685,6 +687,8 @@ wq_status check_sizes(const char *who, int T, const int32_t *rows, const int32_t
     WQ_REQUIRE(T > 0 && R > 0 && E > 0 && N > 0 && K > 0, WQ_ERR_INVALID_ARG,
                "%s: sizes must be positive (T=%d R=%d E=%d N=%d K=%d)", who, T, R, E, N, K);
     WQ_REQUIRE(E <= MAX_E, WQ_ERR_UNSUPPORTED, "%s: E (%d) must be at most %d", who, E, MAX_E);
+    WQ_REQUIRE(T <= MAX_SIZE && R <= MAX_SIZE && K <= MAX_SIZE, WQ_ERR_UNSUPPORTED,
+               "%s: T (%d), R (%d) and K (%d) must be at most %d", who, T, R, K, MAX_SIZE);
     WQ_REQUIRE(rows || R == T, WQ_ERR_INVALID_ARG, "%s: without rows, R (%d) must equal T (%d)", who, R, T);
     WQ_REQUIRE(!swiglu || N % 2 == 0, WQ_ERR_INVALID_ARG, "%s: N (%d) must be even with SwiGLU", who, N);
     WQ_REQUIRE((long long)E * N <= INT_MAX - 4 * BM, WQ_ERR_UNSUPPORTED, "%s: E * N must be below 2^31", who);

@@ -460,8 +460,8 @@ wq_status wq_moe_route(const void *logits, wq_dtype dtype, int T, int E, int top
  *   y[p][n] = round(d[n])                             (swiglu == 0, y [R][N])
  *   y[p][i] = round(silu(d[i]) * d[N/2 + i])          (swiglu != 0, y [R][N/2])
  * with silu(g) = g / (1 + exp(-g)) in fp32 and one rounding.  d per format:
- *   w4a16, w4a16_bf16:  W_e[n][k] = s (q - z), each rounded to the type of x
- *       (fp16, bf16) before the product, fp32 accumulation (order unspecified)
+ *   w4a16, w4a16_bf16:  W_e[n][k] = s (q - z), x and y fp16 or bf16, fp32
+ *       accumulation (order unspecified); rounding of the weights: see below
  *   w8a8:  (float)(int32 sum of codes) * sx[token] * sw[e][n]
  *   fp8:   the same with E4M3 codes and an fp32 sum; sx is [T] or [1]
  *       (sx_per_row), sw [E][N] or [E], one per expert (sw_per_row)
@@ -471,8 +471,13 @@ wq_status wq_moe_route(const void *logits, wq_dtype dtype, int T, int E, int top
  * offsets[E] on are not written.  An entry of rows outside [0, T) gives a row
  * of zeros; offsets outside their range are clamped to it and made
  * non-decreasing, so that no value of either reads or writes out of bounds.
- * A NaN or infinity in a row of x stays in that row of y.
- * E <= 512, E * N < 2^31.  w4a16: group_size in {32, 64, 128, 256}, K a
+ * A NaN or infinity in a row of x stays in that row of y.  y must not overlap
+ * an input.
+ * Rounding of the INT4 weights: with at least 22 rows per expert on average (R
+ * against the experts, or R, whichever are fewer) each s (q - z) is rounded to
+ * the type of x, as in wq_gemm_w4a16; below, it is not: the codes are
+ * multiplied exactly and each group's sum is scaled in fp32.
+ * E <= 512, E * N < 2^31, T, R and K <= 2^29.  w4a16: group_size in {32, 64, 128, 256}, K a
  * multiple of it.  w8a8 and fp8: K % 16 == 0 (w8a8: K <= 131056).  swiglu:
  * N even.
  */

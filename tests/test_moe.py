@@ -77,7 +77,7 @@ def test_w4_refusals(wq, bf):
     assert call(g=96) == una and call(K=192) == inv and call(E=513) == una
     assert call(rows=None) == inv                      # R != T without rows
     assert call(N=63, sw=1) == inv
-    assert call(E=512, N=1 << 23) == una
+    assert call(E=512, N=1 << 23) == una and call(K=1 << 30) == una and call(R=(1 << 29) + 1) == una
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -443,6 +443,57 @@ def test_products_graph_replay_with_new_routing(wq, kind):
         y, tol, written = product_ref(kind, x, w, rows, off.cpu(), R, K, False)
         assert ((out.double() - y).abs() <= tol)[written].all()
         assert (out[~written] == SENTINEL).all()
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("counts", [[3, 9], [70, 50]])
+def test_products_tiny_and_mixed_values(wq, kind, counts):
+    """Subnormal activations and scales, and values near the largest, keep their precision."""
+    N, K, group = 96, 512, 64
+    (q, s, z), _ = make_weights(kind, 2, N, K, group, 6)
+    T = sum(counts)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, K, device="cuda", generator=g)
+    x[: T // 2] *= 2.0 ** -18                            # fp16 subnormals
+    x[T // 2:, ::7] *= 1000.0
+    x = x.to(torch.float16 if kind == "fp16" else torch.bfloat16)
+    s = s.clone()
+    s[0, ::3] = 2.0 ** -20                               # a subnormal fp16 scale
+    codes = ((q.unsqueeze(-1) >> torch.arange(0, 32, 4, device="cuda", dtype=torch.int32)) & 15).view(2, N, K).double()
+    zeros = ((z.unsqueeze(-1) >> torch.arange(0, 32, 4, device="cuda", dtype=torch.int32)) & 15).view(2, N, -1)
+    zeros = zeros[..., :K // group].double().repeat_interleave(group, -1)
+    w = (codes - zeros) * s.double().repeat_interleave(group, -1)
+    off = torch.tensor([0, counts[0], T], dtype=torch.int32, device="cuda")
+    y = wq.grouped_gemm_w4a16(x, q, s, z, off, group_size=group)
+    ref, tol, written = product_ref(kind, x.double(), w, None, off.cpu(), T, K, False)
+    assert ((y.double() - ref).abs() <= tol)[written].all()
+
+
+@gpu
+@pytest.mark.parametrize("kind", FORMATS)
+@pytest.mark.parametrize("counts", [[3, 9, 0, 5], [300, 40, 0, 180]])
+def test_waits_that_run_out_leave_the_context_usable(wq, kind, counts):
+    """Under a limit of a nanosecond the kernels finish or give up; afterwards the same call gives the same result."""
+    N, K = 640, 2048
+    wa, _ = make_weights(kind, 4, N, K, 128, 2)
+    T = sum(counts)
+    xa, _ = make_x(kind, T, K, 2)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    rows = torch.randperm(T, device="cuda").to(torch.int32)
+    good = [call(wq, kind, xa, wa, off, r, 128, False) for r in (rows, None)]
+    assert wq.device_status() == 0
+    try:
+        wq.set_wait_limit(1)
+        for _ in range(3):
+            for r in (rows, None):
+                call(wq, kind, xa, wa, off, r, 128, False)
+        assert wq.device_status() in (wq.WQ_OK, wq.WQ_ERR_TIMEOUT)
+    finally:
+        wq.set_wait_limit(0)
+    for r, y in zip((rows, None), good):
+        assert torch.equal(call(wq, kind, xa, wa, off, r, 128, False), y)
+    assert wq.device_status() == 0
 
 
 @gpu
