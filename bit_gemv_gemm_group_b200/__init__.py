@@ -573,11 +573,14 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, worksp
     T, E = logits.shape
     k = int(top_k)
     cols = max(k, 0)
+    n = (T * cols + 3) & ~3                    # one allocation, every part 16-byte aligned
     new = logits.new_empty
-    ids, slots = new((T, cols), dtype=torch.int32), new((T, cols), dtype=torch.int32)
-    weights = new((T, cols), dtype=torch.float32)
-    offsets = new((E + 1,), dtype=torch.int32)
-    rows = new((T * cols,), dtype=torch.int32)
+    buf = new((4 * n + E + 1,), dtype=torch.int32)
+    ids = buf.as_strided((T, cols), (cols, 1), 0)
+    weights = buf.view(torch.float32).as_strided((T, cols), (cols, 1), n)
+    slots = buf.as_strided((T, cols), (cols, 1), 2 * n)
+    rows = buf.as_strided((T * cols,), (1,), 3 * n)
+    offsets = buf.as_strided((E + 1,), (1,), 4 * n)
     need = lib.wq_moe_route_workspace_bytes(T, E)
     if workspace is None:
         workspace = new((need,), dtype=torch.uint8) if need else None
