@@ -129,6 +129,41 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 // rounding that follows.
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
+// Two values rounded to fp16 or bf16, the first in the low half: one instruction, where a conversion of a single
+// value takes the quarter-rate pipe.
+template <bool BF>
+__device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
+    uint32_t d;
+    if (BF) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// Stores v[0 .. count) down a column of y: rows `step` elements apart.  `full` (the same in the whole warp): all of
+// them, without a test per row.
+template <bool BF, int N>
+__device__ __forceinline__ void store_column(uint16_t *y, size_t step, const float (&v)[N], int count, bool full) {
+    if (full) {
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+            const uint32_t h = round_pair<BF>(v[j], v[j + 1]);
+            *y = (uint16_t)h;
+            y += step;
+            *y = (uint16_t)(h >> 16);
+            y += step;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+            const uint32_t h = round_pair<BF>(v[j], v[j + 1]);
+            if (j < count) *y = (uint16_t)h;
+            y += step;
+            if (j + 1 < count) *y = (uint16_t)(h >> 16);
+            y += step;
+        }
+    }
+}
+
 // Clusters of `size` CTAs of a kernel that are resident at once (one CTA per SM; some GPCs have SMs left over), at
 // least 1.  A persistent grid of more clusters would run the rest after the others have finished.
 template <typename Kernel>

@@ -102,11 +102,6 @@ __device__ __forceinline__ uint4 permute_x(uint4 v) {
                       prmt(v.y, v.w, 0x7632u));
 }
 
-template <bool BF>
-__device__ __forceinline__ uint16_t round_bits(float v) {
-    return BF ? float_to_bf16_bits_rn(v) : float_to_half_bits_rn(v);
-}
-
 // The part of a tile's depth that CTA `rank` of `split` takes: stages [s0, s1), in whole packed tiles.
 struct Depth {
     int s0, s1;
@@ -379,21 +374,27 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int col = cur.n0 + (SWIGLU ? 16 * q + (lane & 15) : 32 * q + lane);
             const bool col_ok = col < a.ldy;
             uint16_t *yt = a.y + (size_t)cur.r0 * a.ldy + col;
+            const bool full = cur.rows == BR && __all_sync(0xffffffffu, col_ok);
             if (SWIGLU) {
                 const bool up = lane >= 16;   // this lane's weight row is an up row
+                float o[BR / 2];
 #pragma unroll
                 for (int j = 0; j < BR; j += 2) {
                     const float other = __shfl_xor_sync(0xffffffffu, up ? acc[j] : acc[j + 1], 16);
-                    const float g = up ? other : acc[j], l = up ? acc[j + 1] : other;
-                    const int row = j + (up ? 1 : 0);
-                    if (row < cur.rows && col_ok)
-                        yt[(size_t)row * a.ldy] = (zero_rows >> row) & 1 ? (uint16_t)0 : round_bits<BF>(swiglu(g, l));
+                    o[j / 2] = swiglu(up ? other : acc[j], up ? acc[j + 1] : other);
                 }
-            } else {
+                if (zero_rows)
 #pragma unroll
-                for (int j = 0; j < BR; ++j)
-                    if (j < cur.rows && col_ok)
-                        yt[(size_t)j * a.ldy] = (zero_rows >> j) & 1 ? (uint16_t)0 : round_bits<BF>(acc[j]);
+                    for (int j = 0; j < BR / 2; ++j)
+                        if ((zero_rows >> (2 * j + (up ? 1 : 0))) & 1) o[j] = 0.0f;
+                store_column<BF>(yt + (up ? a.ldy : 0), 2 * (size_t)a.ldy, o,
+                                 col_ok ? (cur.rows + (up ? 0 : 1)) / 2 : 0, full);
+            } else {
+                if (zero_rows)
+#pragma unroll
+                    for (int j = 0; j < BR; ++j)
+                        if ((zero_rows >> j) & 1) acc[j] = 0.0f;
+                store_column<BF>(yt, (size_t)a.ldy, acc, col_ok ? cur.rows : 0, full);
             }
         }
     } else {

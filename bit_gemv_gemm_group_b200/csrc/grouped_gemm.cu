@@ -162,11 +162,6 @@ __device__ __forceinline__ uint4 dequant_word(uint32_t w, uint32_t magic, const 
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-template <Kind KIND>
-__device__ __forceinline__ uint16_t out_bits(float v) {
-    return KIND == K_W4B ? float_to_bf16_bits_rn(v) : float_to_half_bits_rn(v);
-}
-
 // SWIGLU: a CTA's 128 weight rows are, per 32 TMEM lanes, 16 gate rows and the 16 up rows that belong to
 // them, so gate and up of one output meet by a shuffle inside a warp.
 template <Kind KIND, bool GATHER, bool SWIGLU, bool PAIR>
@@ -387,7 +382,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                 asm volatile("bar.sync 1, %0;" ::"n"(ET) : "memory");
             }
             const int col = w.n0 + rank * BNC + (SWIGLU ? 16 * q + (lane & 15) : 32 * q + lane);
-            const bool col_ok = col < a.ldy;
+            const bool col_ok = col < a.ldy, cols_ok = __all_sync(0xffffffffu, col_ok);
             float sw = 1.0f;
             if (!W4)
                 sw = a.sw_per_row ? __ldg(a.sw + min((size_t)a.E * a.N - 1,
@@ -405,43 +400,39 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                 const uint32_t zero = GATHER ? bad[c / 32] : 0u;
                 const int left = w.rows - c;
                 uint16_t *yt = a.y + (size_t)(w.r0 + c) * a.ldy + col;
-                // Values in place of the accumulators, scaled.
+                const bool full = left >= 32 && cols_ok;
+                float v[32];
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
-                    if (W4) continue;
-                    const float4 sx = *reinterpret_cast<const float4 *>(sxs + c + j);
-                    const float sv[4] = {sx.x, sx.y, sx.z, sx.w};
+                    float sv[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+                    if (!W4) *reinterpret_cast<float4 *>(sv) = *reinterpret_cast<const float4 *>(sxs + c + j);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float f = KIND == K_I8 ? (float)(int32_t)r[j + i] : __uint_as_float(r[j + i]);
-                        r[j + i] = __float_as_uint(__fmul_rn(__fmul_rn(f, sv[i]), sw));
+                        v[j + i] = W4 ? f : __fmul_rn(__fmul_rn(f, sv[i]), sw);
                     }
                 }
                 if (SWIGLU) {
                     // Lanes 0-15 hold gate rows and keep the even rows of y, lanes 16-31 up rows and the odd ones.
                     const bool up = lane >= 16;
-                    yt += up ? a.ldy : 0;
+                    float o[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        const uint32_t other = __shfl_xor_sync(0xffffffffu, up ? r[j] : r[j + 1], 16);
-                        const float g = __uint_as_float(up ? other : r[j]), l = __uint_as_float(up ? r[j + 1] : other);
-                        r[j] = out_bits<KIND>(swiglu(g, l));
+                        const float other = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 16);
+                        o[j / 2] = swiglu(up ? other : v[j], up ? v[j + 1] : other);
                     }
                     if (zero)
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2)
-                            if ((zero >> (j + (up ? 1 : 0))) & 1) r[j] = 0;
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2)
-                        if (j + (up ? 1 : 0) < left && col_ok) yt[(size_t)j * a.ldy] = (uint16_t)r[j];
+                        for (int j = 0; j < 16; ++j)
+                            if ((zero >> (2 * j + (up ? 1 : 0))) & 1) o[j] = 0.0f;
+                    store_column<KIND == K_W4B>(yt + (up ? a.ldy : 0), 2 * (size_t)a.ldy, o,
+                                                col_ok ? (left + (up ? 0 : 1)) / 2 : 0, full);
                 } else {
                     if (zero)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if ((zero >> j) & 1) r[j] = 0;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j < left && col_ok) yt[(size_t)j * a.ldy] = out_bits<KIND>(__uint_as_float(r[j]));
+                            if ((zero >> j) & 1) v[j] = 0.0f;
+                    store_column<KIND == K_W4B>(yt, (size_t)a.ldy, v, col_ok ? left : 0, full);
                 }
             }
             tc_fence_before();
