@@ -2,6 +2,8 @@
 // offsets in device memory, and small device helpers.
 #pragma once
 
+#include <atomic>
+
 #include "sm100.cuh"
 #include "wq_device.cuh"
 #include "wq_host.h"
@@ -162,6 +164,19 @@ __device__ __forceinline__ void store_column(uint16_t *y, size_t step, const flo
             y += step;
         }
     }
+}
+
+// Lets `kern` use `smem` bytes of shared memory, once per device (`done`: a bit each).
+template <typename Kernel>
+wq_status allow_smem(Kernel kern, size_t smem, std::atomic<uint64_t> &done, const char *who) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (e == cudaSuccess && (done.load(std::memory_order_acquire) & bit)) return WQ_OK;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return fail(WQ_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", who, cudaGetErrorString(e));
+    done.fetch_or(bit, std::memory_order_release);
+    return WQ_OK;
 }
 
 // Clusters of `size` CTAs of a kernel that are resident at once (one CTA per SM; some GPCs have SMs left over), at

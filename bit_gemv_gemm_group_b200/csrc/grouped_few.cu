@@ -539,9 +539,9 @@ int choose_split(long long tiles, int K, const int (&clusters)[3]) {
 template <bool BF, bool SWIGLU>
 wq_status launch(const CUtensorMap &tw, const Args &a, long long tiles, cudaStream_t st, const char *who) {
     auto kern = few_rows_kernel<BF, SWIGLU>;
-    cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(MAX_SPLIT, MAX_E));
-    if (e != cudaSuccess) return fail(WQ_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", who, cudaGetErrorString(e));
+    static std::atomic<uint64_t> allowed{0};
+    const wq_status ok = allow_smem(kern, smem_bytes(MAX_SPLIT, MAX_E), allowed, who);
+    if (ok != WQ_OK) return ok;
     // Looked up once: every device of the library's kind answers the same.
     static const int clusters[3] = {num_sms(), resident_clusters(kern, THREADS, smem_bytes(2, MAX_E), 2),
                                     resident_clusters(kern, THREADS, smem_bytes(4, MAX_E), 4)};
@@ -559,7 +559,7 @@ wq_status launch(const CUtensorMap &tw, const Args &a, long long tiles, cudaStre
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, tw, a, split);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tw, a, split);
     if (e != cudaSuccess) return fail(WQ_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return WQ_OK;
 }

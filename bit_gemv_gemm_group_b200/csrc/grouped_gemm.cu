@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
-        prefetch_tmap(&tmap_x);
+        if (!GATHER) prefetch_tmap(&tmap_x);
         prefetch_tmap(&tmap_w);
     }
     if (warp == 1) build_table<BR>(a, off, tiles, lane);
@@ -585,8 +585,9 @@ wq_status launch(const CUtensorMap &tx, const CUtensorMap &tw, const Args &a, lo
     using L = Layout<KIND, GATHER, PAIR>;
     auto kern = grouped_gemm_kernel<KIND, GATHER, SWIGLU, PAIR>;
     const size_t smem = L::smem(a.E);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::smem(MAX_E));
-    if (e != cudaSuccess) return fail(WQ_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", who, cudaGetErrorString(e));
+    static std::atomic<uint64_t> allowed{0};
+    const wq_status ok = allow_smem(kern, L::smem(MAX_E), allowed, who);
+    if (ok != WQ_OK) return ok;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(L::THREADS);
     cfg.dynamicSmemBytes = smem;
@@ -600,7 +601,7 @@ wq_status launch(const CUtensorMap &tx, const CUtensorMap &tw, const Args &a, lo
     cfg.numAttrs = 1;
     const int units = PAIR ? num_sms() / 2 : num_sms();
     cfg.gridDim = dim3((unsigned)std::min<long long>(units, most_tiles) * (PAIR ? 2 : 1));
-    e = cudaLaunchKernelEx(&cfg, kern, tx, tw, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tx, tw, a);
     if (e != cudaSuccess) return fail(WQ_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return WQ_OK;
 }
@@ -624,11 +625,11 @@ wq_status dispatch(const void *w, Args a, bool swiglu, cudaStream_t st, const ch
     WQ_REQUIRE(most < INT_MAX / 2, WQ_ERR_UNSUPPORTED, "%s: R (%d) x N (%d) gives too many tiles", who, a.R, a.N);
     const bool gather = a.rows != nullptr;
     constexpr int W_BYTES = W4 ? P_ROW : STAGE_K;   // of a weight row per copy
-    CUtensorMap tx, tw;
+    CUtensorMap tx = {}, tw;   // tx: not used by gathered rows
     const CUtensorMapDataType xt = KIND == K_W4H ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                  : KIND == K_W4B ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const int xb = W4 ? 2 : 1;
-    if (!encode_tmap_2d(&tx, xt, xb, a.x, (uint64_t)a.K, (uint64_t)a.T, (uint64_t)a.K * xb, STAGE_K / xb,
+    if (!gather && !encode_tmap_2d(&tx, xt, xb, a.x, (uint64_t)a.K, (uint64_t)a.T, (uint64_t)a.K * xb, STAGE_K / xb,
                         Layout<KIND, false, PAIR>::BOX,
                         CU_TENSOR_MAP_SWIZZLE_128B))
         return WQ_ERR_CUDA;
