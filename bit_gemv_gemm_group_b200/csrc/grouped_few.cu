@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool ok = true;
         for (int t = first; ok && get_tile<BN, BR, BR>(a, off, tiles, t, w); t += stride) {
             for (int sb = dep.s0; sb < dep.s1; sb += 2, ++it) {
-                ok = wait_parity(smem_u32(&bar->pk_empty[p]), ph, ctl, SITE_PACKED);
+                ok = wait_parity_lean(smem_u32(&bar->pk_empty[p]), ph, ctl, SITE_PACKED);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 if (leader) {
                     const uint32_t fb = smem_u32(&bar->pk_full[p]), dst = sP + p * P_BYTES;
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const uint32_t it = 2 * (pk + b) + h, s = it % STAGES, u = it / STAGES;
                     const uint32_t fb = smem_u32(&bar->full[s]);
                     ok = h == 0 ? wait_parity2(ae, (cu & 1) ^ 1, fb, u & 1, ctl, SITE_MMA)
-                                : wait_parity(fb, u & 1, ctl, SITE_MMA);
+                                : wait_parity_lean(fb, u & 1, ctl, SITE_MMA);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     tc_fence_after();
                     if (leader) {
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         load(g_first);
                     }
                 }
-                ok = wait_parity(smem_u32(&bar->acc_full[c]), (pk / accs) & 1, ctl, SITE_SCALE);
+                ok = wait_parity_lean(smem_u32(&bar->acc_full[c]), (pk / accs) & 1, ctl, SITE_SCALE);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
                 const uint32_t sp[4] = {sc.x, sc.y, sc.z, sc.w};
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // and loads are contiguous.
                 if (rank != 0) {
                     if (n > 0) {
-                        ok = wait_parity(smem_u32(&bar->red_free[q]), (n - 1) & 1, ctl, SITE_SPLIT);
+                        ok = wait_parity_lean(smem_u32(&bar->red_free[q]), (n - 1) & 1, ctl, SITE_SPLIT);
                         if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     }
                     const uint32_t dst = mapa_shared(sR + (rank - 1) * RED_BYTES + trow * 4, 0);
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bar->red_full[q]), 0));
                     continue;
                 }
-                ok = wait_parity(smem_u32(&bar->red_full[q]), n & 1, ctl, SITE_SPLIT);
+                ok = wait_parity_lean(smem_u32(&bar->red_full[q]), n & 1, ctl, SITE_SPLIT);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 fence_cluster();
                 for (int c = 0; c < split - 1; ++c) {
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                     if (h == 0) {
-                        ok = wait_parity(eb + 8, ep, ctl, SITE_DEQUANT);
+                        ok = wait_parity_lean(eb + 8, ep, ctl, SITE_DEQUANT);
                         if (!(ok = __all_sync(0xffffffffu, ok))) break;
                         tc_fence_after();
 #pragma unroll

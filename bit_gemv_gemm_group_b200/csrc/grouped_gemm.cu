@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                 for (int kb = 0; kb < kst; ++kb, ++it) {
                     const uint32_t s = it % STAGES, u = it / STAGES;
                     const uint32_t fb = smem_u32(&bar->full[s]);
-                    ok = wait_parity(smem_u32(&bar->empty[s]), (u & 1) ^ 1, ctl, SITE_PRODUCER);
+                    ok = wait_parity_lean(smem_u32(&bar->empty[s]), (u & 1) ^ 1, ctl, SITE_PRODUCER);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     if (leader) {
                         mbar_arrive_expect_tx(fb, bytes);
@@ -290,12 +290,12 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
             const uint32_t acc = n & 1, d = tmem_base + acc * BR;
             const uint32_t idesc = idesc_rows<KIND>(PAIR ? 2 * BM : BM, local_rows(w) * (PAIR ? 2 : 1));
             if (rank == 0) {
-                ok = wait_parity(smem_u32(&bar->acc_empty[acc]), ((n >> 1) & 1) ^ 1, ctl, SITE_MMA);
+                ok = wait_parity_lean(smem_u32(&bar->acc_empty[acc]), ((n >> 1) & 1) ^ 1, ctl, SITE_MMA);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
             }
             for (int kb = 0; kb < kst; ++kb) {
-                ok = (!TMA_STAGE || wait_parity(smem_u32(&bar->full[s]), ph, ctl, SITE_MMA)) &&
-                     (!(rank == 0 ? PUT0 : PUT1) || wait_parity(smem_u32(&bar->put[s]), ph, ctl, SITE_MMA));
+                ok = (!TMA_STAGE || wait_parity_lean(smem_u32(&bar->full[s]), ph, ctl, SITE_MMA)) &&
+                     (!(rank == 0 ? PUT0 : PUT1) || wait_parity_lean(smem_u32(&bar->put[s]), ph, ctl, SITE_MMA));
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
                 if (GATHER) fence_proxy_async_smem();  // rows copied by cp.async, read by the tensor cores
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
         for (int t = first; ok && get_tile<BN, BR, STEP>(a, off, tiles, t, w); t += stride) {
             for (int b = 0; b < packs; ++b, ++it) {
                 const uint32_t p = it % PSTAGES, u = it / PSTAGES;
-                ok = wait_parity(smem_u32(&bar->pk_empty[p]), (u & 1) ^ 1, ctl, SITE_PACKED);
+                ok = wait_parity_lean(smem_u32(&bar->pk_empty[p]), (u & 1) ^ 1, ctl, SITE_PACKED);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 if (leader) {
                     const uint32_t fb = smem_u32(&bar->pk_full[p]);
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                                                      (size_t)weight_row(w, 2 * q + (lane >> 4)) + (lane & 15)))
                                   : __ldg(a.sw + w.e);
             // After a wait has run out the warps still walk the tiles, so that all meet at the barrier.
-            ok = ok && wait_parity(smem_u32(&bar->acc_full[acc]), u & 1, ctl, SITE_EPILOGUE);
+            ok = ok && wait_parity_lean(smem_u32(&bar->acc_full[acc]), u & 1, ctl, SITE_EPILOGUE);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) continue;
             tc_fence_after();
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
             }
             for (int kb = 0; kb < kst; ++kb, ++it) {
                 const uint32_t s = it % STAGES, u = it / STAGES;
-                ok = wait_parity(smem_u32(&bar->empty[s]), (u & 1) ^ 1, ctl, SITE_GATHER);
+                ok = wait_parity_lean(smem_u32(&bar->empty[s]), (u & 1) ^ 1, ctl, SITE_GATHER);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const uint32_t dst = dst0 + s * L::B_BYTES;
                 const bool in = kb * STAGE_K + c * 16 < (int)pitch;   // false only past the end of the depth
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                         gc.set((i & 1) ? s2 >> 16 : s2 & 0xFFFFu, (cz >> (4 * (g & 7))) & 0xFu);
                     }
                     if (h == 2) {
-                        ok = wait_parity(eb + 8, ph ^ 1, ctl, SITE_DEQUANT);
+                        ok = wait_parity_lean(eb + 8, ph ^ 1, ctl, SITE_DEQUANT);
                         if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     }
                     const uint32_t words[4] = {v[h].x, v[h].y, v[h].z, v[h].w};

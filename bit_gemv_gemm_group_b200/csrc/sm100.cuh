@@ -105,11 +105,29 @@ __device__ __forceinline__ bool wait_parity(uint32_t bar, uint32_t parity, const
     }
 }
 
+// wait_parity for kernels whose other warps need the issue slots: the abort flag and the clock, about 20
+// instructions, are looked at after every 16th test only.
+__device__ __forceinline__ bool wait_parity_lean(uint32_t bar, uint32_t parity, const WaitCtl &c, unsigned site) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*c.abort) return false;
+        if (globaltimer() - t0 > c.limit_ns) {
+            *c.abort = 1;
+            atomicOr(c.status, site);
+            return false;
+        }
+    }
+}
+
 // Waits for a phase of each of two barriers, testing both at once: a test takes about 100 cycles to answer.
 __device__ __forceinline__ bool wait_parity2(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
                                              const WaitCtl &c, unsigned site) {
     const bool b0 = mbar_try_wait(bar0, parity0), b1 = mbar_try_wait(bar1, parity1);
-    return (b0 || wait_parity(bar0, parity0, c, site)) && (b1 || wait_parity(bar1, parity1, c, site));
+    return (b0 || wait_parity_lean(bar0, parity0, c, site)) && (b1 || wait_parity_lean(bar1, parity1, c, site));
 }
 
 // Drain wait used on the way out: same, but ignores the abort flag.
