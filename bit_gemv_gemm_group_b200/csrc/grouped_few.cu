@@ -22,6 +22,13 @@
 //   warps 8-15   two groups of four warps, every other pack each: rows of x into shared memory, and codes ->
 //                q - z into tensor memory.  A thread takes 256 codes at a time: with 128 (and twice the warps)
 //                its waits, loads and addresses were 250 of 390 instructions
+//
+// Measured on B200: 2 of 8 experts of 28672 x 4096 for one token, 122 MB, 53.7 us (2.3 TB/s; 51 us of them in the
+// four CTAs that take a fourth tile of the 448, the others are done after 40), 8 experts for 16 rows, 440 MB,
+// 148 us (3.0 TB/s); 64 experts of 4096 x 2048 for 192 bf16 rows, groups of 64, 103 us (2.7 TB/s).  With the whole
+// dequantization, the fmas, all but one MMA per stage and the loads of x and scales taken out the second takes
+// 94 us: no unit bounds it alone, the loop of a dequantizing group (two thirds of its 1290 cycles per pack are
+// arithmetic at about 5 cycles an instruction) and the rest of the pipeline lie close together.
 #include "grouped.cuh"
 
 #include <algorithm>
@@ -39,7 +46,7 @@ constexpr int STAGES = 4, P_SLOTS = 8, MAX_ACCS = 8;
 constexpr uint32_t X_ATOM = BR * 128, X_BYTES = 2 * X_ATOM;   // 64 values a row and atom
 constexpr uint32_t P_BYTES = BM * 128;      // a pack: 256 codes of 128 rows, two stages
 constexpr uint32_t A_COLS = SK / 2;         // tensor memory columns of a stage
-constexpr int THREADS = 512, SCALE_WARP0 = 4, DQ_WARP0 = 8;
+constexpr int THREADS = 512, DQ_WARP0 = 8;
 constexpr int MAX_SPLIT = 4;
 constexpr uint32_t OFF_X = P_SLOTS * P_BYTES;
 constexpr uint32_t OFF_RED = OFF_X + STAGES * X_BYTES;    // not used when the tile is not split
@@ -49,8 +56,8 @@ constexpr unsigned SITE_PACKED = 0x2001, SITE_MMA = 0x2002, SITE_SCALE = 0x2008,
 
 // Tensor memory: four stages of 64 columns, then accumulators, 16 columns per group and 256 / gs groups per pack.
 // Pack, stage and accumulator slots belong to one dequantizing group and one issuer each (an even number of
-// packs, 4 stages, an even number of accumulators): a thread that waited for a slot another one had not used yet could take an older phase of
-// its barrier, of the same parity, for the one it waits for.
+// packs, 4 stages, an even number of accumulators): a thread that waited for a slot that another one had not
+// used yet could take an older phase of its barrier, of the same parity, for the one it waits for.
 static_assert(STAGES * A_COLS + 256 * BR / 16 <= 512, "tensor memory");
 
 struct Bars {
@@ -249,8 +256,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             drain_parity(smem_u32(&bar->drain[me]), 0, DRAIN_NS, a.status, SITE_DRAIN);
         }
         __syncwarp();
-    } else if (warp == 3) {
-    } else if (warp < DQ_WARP0) {
+    } else if (warp >= 4 && warp < DQ_WARP0) {
         // -------------------------------------------------------------------- scales, end of the tile
         const int q = warp & 3, trow = 32 * q + lane;   // TMEM lanes 32 q ..; this lane's row of the tile
         const uint32_t t_row = tmem + ((uint32_t)(32 * q) << 16);
@@ -397,7 +403,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 store_column<BF>(yt, (size_t)a.ldy, acc, col_ok ? cur.rows : 0, full);
             }
         }
-    } else {
+    } else if (warp >= DQ_WARP0) {
         // -------------------------------------------------------------------- codes -> q - z
         // Group d takes every other pack and fills stages 2 d and 2 d + 1; a thread takes one weight row.
         const int q = warp & 3, trow = 32 * q + lane, d = (warp - DQ_WARP0) >> 2;

@@ -29,6 +29,12 @@
 //   then        four warps that gather indexed activation rows by cp.async (TMA's gather of four rows a
 //               request took 32 cycles for its 512 bytes, four times what the MMAs leave), and for INT4
 //               three groups of four warps that dequantize every third packed tile each
+//
+// Measured on B200, 16384 rows over 32 experts of 4096 x 4096 (0.55 T products, at clocks that the power cap has
+// brought down): INT8 with SwiGLU 234 us (2.35 POPS, 0.69 of twice the bf16 burst rate and 0.81 of twice the
+// sustained one), INT4 with bf16 rows 489 us (1.12 PFLOP/s, 0.77 of the sustained rate; 443 us where the rows
+// already lie in order, 388 us without the dequantization's arithmetic).  16 rows over 8 INT8 experts of
+// 4096 x 14336, 466 MB: 78 us (6.0 TB/s, 0.93 of the copy rate).
 #include "grouped.cuh"
 
 #include <algorithm>
