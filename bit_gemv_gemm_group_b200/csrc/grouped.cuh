@@ -127,6 +127,47 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     return v;
 }
 
+// q - z of the 8 codes of a word as fp16 or bf16 pairs, in the order 0, 4, 1, 5, 2, 6, 3, 7 in which masks of
+// the word leave them (x is taken in the same order, see permute_x): the integer pipe, which runs at half
+// the issue rate, is the busiest one of the kernels that do this, and in k order each pair would take a byte permutation more.
+// fp16: masked nibbles under the exponent of 1024 read 1024 + q (low nibbles) and 1024 + 16 q (high ones).
+// bf16: 128 + q has 8 bits, so every nibble is shifted down first.
+template <bool BF>
+struct Zero {
+    uint32_t lo, hi;   // fp16: -(1024 + z) and -(64 + z); bf16: -(128 + z)
+    __device__ __forceinline__ explicit Zero(uint32_t z)
+        : lo((BF ? 0xC300C300u : 0xE400E400u) + z * 0x00010001u), hi(0xD400D400u + z * 0x00100010u) {}
+    // From 16 bits of a register whose lower half is free for something else.
+    static __device__ __forceinline__ uint32_t pack(uint32_t z) { return ((BF ? 0xC300u : 0xE400u) + z) << 16; }
+    static __device__ __forceinline__ Zero unpack(uint32_t v) {
+        Zero r(0);
+        r.lo = prmt(v, 0u, 0x3232u);
+        r.hi = r.lo * 16u + (0xD400D400u - 0xE400E400u * 16u);
+        return r;
+    }
+};
+
+template <bool BF>
+__device__ __forceinline__ void code_word(uint32_t w, uint32_t magic, const Zero<BF> &z, uint32_t *o) {
+    if (BF) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(mask_or(w >> (4 * i), 0x000F000Fu, magic)), "r"(z.lo));
+    } else {
+        const uint32_t w8 = w >> 8;
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[0]) : "r"(mask_or(w, 0x000F000Fu, magic)), "r"(z.lo));
+        o[1] = hfma2(mask_or(w, 0x00F000F0u, magic), 0x2C002C00u, z.hi);
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[2]) : "r"(mask_or(w8, 0x000F000Fu, magic)), "r"(z.lo));
+        o[3] = hfma2(mask_or(w8, 0x00F000F0u, magic), 0x2C002C00u, z.hi);
+    }
+}
+
+// Eight values of x in the order of code_word.
+__device__ __forceinline__ uint4 permute_x(uint4 v) {
+    return make_uint4(prmt(v.x, v.z, 0x5410u), prmt(v.x, v.z, 0x7632u), prmt(v.y, v.w, 0x5410u),
+                      prmt(v.y, v.w, 0x7632u));
+}
+
 // silu(g) u.  The fast exponential and division are off by a few fp32 units, far below the 16-bit
 // rounding that follows.
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
@@ -207,8 +248,11 @@ int resident_clusters(Kernel kern, int threads, size_t smem, int size) {
 // 4 x 2 x 16 rows is 16 gate rows, their 16 up rows, and so on; otherwise boxes of 16 rows.
 bool encode_weights(CUtensorMap *map, const void *w, uint64_t row_bytes, int width, Args &a, bool swiglu);
 
-// INT4 weights and at most a few dozen rows per expert (grouped_few.cu); `bf16`: type of x and y.
+// INT4 weights and 6 to 22 rows per expert (grouped_few.cu); `bf16`: type of x and y.
 wq_status few_rows_w4(const void *w, Args a, bool bf16, bool swiglu, cudaStream_t st, const char *who);
+
+// INT4 weights and a handful of rows per expert (grouped_stream.cu).
+wq_status stream_rows_w4(const void *w, Args a, bool bf16, bool swiglu, cudaStream_t st, const char *who);
 
 }  // namespace grouped
 }  // namespace wq

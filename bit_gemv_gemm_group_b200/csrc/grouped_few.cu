@@ -1,4 +1,4 @@
-// Expert products with INT4 weights for few rows per expert (decode batches): the same products as
+// Expert products with INT4 weights for few rows per expert (decode batches, 6 to 22): the same products as
 // grouped_gemm.cu's kernel, whose tiles these are, organised around the stream of packed weights.
 //
 //   y[p][n] = sum_j s[n][j] * ( sum_{k in group j} (q[n][k] - z[n][j]) x[rows[p]][k] )
@@ -23,12 +23,11 @@
 //                q - z into tensor memory.  A thread takes 256 codes at a time: with 128 (and twice the warps)
 //                its waits, loads and addresses were 250 of 390 instructions
 //
-// Measured on B200: 2 of 8 experts of 28672 x 4096 for one token, 122 MB, 53.7 us (2.3 TB/s; 51 us of them in the
-// four CTAs that take a fourth tile of the 448, the others are done after 40), 8 experts for 16 rows, 440 MB,
-// 148 us (3.0 TB/s); 64 experts of 4096 x 2048 for 192 bf16 rows, groups of 64, 103 us (2.7 TB/s).  With the whole
-// dequantization, the fmas, all but one MMA per stage and the loads of x and scales taken out the second takes
-// 94 us: no unit bounds it alone, the loop of a dequantizing group (two thirds of its 1290 cycles per pack are
-// arithmetic at about 5 cycles an instruction) and the rest of the pipeline lie close together.
+// Measured on B200: 8 experts of 28672 x 4096 for 64 rows, fp16, 492 MB, 154 us (3.2 TB/s); 64 experts of
+// 4096 x 2048 for 768 bf16 rows, groups of 64, 297 MB, 146 us (2.0 TB/s).  With the whole dequantization, the fmas,
+// all but one MMA per stage and the loads of x and scales taken out, 440 MB of weights take 94 us against 148: no
+// unit bounds it alone, the loop of a dequantizing group (two thirds of its 1290 cycles per pack are arithmetic
+// at about 5 cycles an instruction) and the rest of the pipeline lie close together.
 #include "grouped.cuh"
 
 #include <algorithm>
@@ -75,39 +74,6 @@ constexpr size_t smem_bytes(int split, int E) {
 }
 
 static_assert(smem_bytes(MAX_SPLIT, MAX_E) <= 232448 && sizeof(Bars) <= 1024, "shared memory");
-
-// q - z of the 8 codes of a word as fp16 or bf16 pairs, in the order 0, 4, 1, 5, 2, 6, 3, 7 in which masks of
-// the word leave them (x is stored in the same order, see permute_x): the integer pipe, which runs at half
-// the issue rate, bounds this loop, and in k order each pair would take a byte permutation more.
-// fp16: masked nibbles under the exponent of 1024 read 1024 + q (low nibbles) and 1024 + 16 q (high ones).
-// bf16: 128 + q has 8 bits, so every nibble is shifted down first.
-template <bool BF>
-struct Zero {
-    uint32_t lo, hi;   // fp16: -(1024 + z) and -(64 + z); bf16: -(128 + z)
-    __device__ __forceinline__ explicit Zero(uint32_t z)
-        : lo((BF ? 0xC300C300u : 0xE400E400u) + z * 0x00010001u), hi(0xD400D400u + z * 0x00100010u) {}
-};
-
-template <bool BF>
-__device__ __forceinline__ void code_word(uint32_t w, uint32_t magic, const Zero<BF> &z, uint32_t *o) {
-    if (BF) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(mask_or(w >> (4 * i), 0x000F000Fu, magic)), "r"(z.lo));
-    } else {
-        const uint32_t w8 = w >> 8;
-        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[0]) : "r"(mask_or(w, 0x000F000Fu, magic)), "r"(z.lo));
-        o[1] = hfma2(mask_or(w, 0x00F000F0u, magic), 0x2C002C00u, z.hi);
-        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[2]) : "r"(mask_or(w8, 0x000F000Fu, magic)), "r"(z.lo));
-        o[3] = hfma2(mask_or(w8, 0x00F000F0u, magic), 0x2C002C00u, z.hi);
-    }
-}
-
-// Eight values of x in the order of code_word.
-__device__ __forceinline__ uint4 permute_x(uint4 v) {
-    return make_uint4(prmt(v.x, v.z, 0x5410u), prmt(v.x, v.z, 0x7632u), prmt(v.y, v.w, 0x5410u),
-                      prmt(v.y, v.w, 0x7632u));
-}
 
 // The part of a tile's depth that CTA `rank` of `split` takes: stages [s0, s1), in whole packed tiles.
 struct Depth {

@@ -393,6 +393,150 @@ def test_fp8_scalar_scales(wq):
         assert ((y.double() - ref).abs() <= tol)[written].all()
 
 
+# INT4 by rows per expert: fewer than 6 on average, and below 22.  N for E experts such that there are tiles enough for
+# each of the shapes that the first of them takes.
+HANDFUL = [1, 8, 0, 9, 3, 2, 17, 1]
+FEW = [9, 0, 40, 7]
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("group,K", [(32, 32), (32, 416), (64, 1088), (128, 128), (128, 1152), (256, 1280), (256, 2304)])
+@pytest.mark.parametrize("N,swiglu", [(70, False), (62, True), (1250, False), (1262, True), (4757, False), (4802, True)])
+def test_products_of_a_handful_of_rows(wq, kind, group, K, N, swiglu):
+    check_product(wq, kind, HANDFUL, T=40, N=N, K=K, group=group, swiglu=swiglu)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("N", [70, 1250, 4757])
+def test_a_handful_of_rows_in_order_and_bad_ones(wq, kind, N):
+    check_product(wq, kind, HANDFUL, T=40, N=N, K=480, gather=False)
+    check_product(wq, kind, HANDFUL, T=40, N=N, K=480, start=2, spare=3)
+    check_product(wq, kind, HANDFUL, T=40, N=N, K=480, bad=True)
+    check_product(wq, kind, HANDFUL, T=1, N=N + N % 2, K=480, bad=True, swiglu=True)
+    check_product(wq, kind, [0] * 300 + [1] + [0] * 211, T=3, N=N, K=64)        # the most experts
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("group,K", [(32, 416), (64, 1088), (128, 2304), (256, 1280)])
+@pytest.mark.parametrize("N,swiglu", [(200, False), (200, True)])
+def test_products_of_few_rows(wq, kind, group, K, N, swiglu):
+    check_product(wq, kind, FEW, T=40, N=N, K=K, group=group, swiglu=swiglu)
+    check_product(wq, kind, FEW, T=40, N=N, K=K, group=group, swiglu=swiglu, bad=True, spare=3)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+def test_a_handful_of_rows_with_bad_offsets(wq, kind):
+    R, E, N, K = 40, 8, 64, 128
+    wa, w = make_weights(kind, E, N, K, 32, 3)
+    xa, x = make_x(kind, R, K, 3)
+    for raw in ([-7, 10, 5, 2000, 30, 1, 2, 3, 4], [50, 60, 70, 80, 90, 1, 1, 1, 1], [0, -1, -2, -3, 9, 9, 8, 7, 2 ** 31 - 1]):
+        fixed = np.maximum.accumulate(np.clip(raw, 0, R))
+        off = torch.tensor(raw, dtype=torch.int32, device="cuda")
+        out = torch.full((R, N), SENTINEL, dtype=xa[0].dtype, device="cuda")
+        call(wq, kind, xa, wa, off, None, 32, False, out)
+        y, tol, written = product_ref(kind, x, w, None, fixed, R, K, False)
+        assert ((out.double() - y).abs() <= tol)[written].all()
+        assert (out[~written] == SENTINEL).all()
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("counts", [[5, 1, 3, 0], [20, 2, 9, 0]])
+def test_nan_and_inf_beside_few_rows(wq, kind, counts):
+    """A row's NaN or infinity stays in its sums, also when it is row 0 and other indices lie outside x."""
+    N, K, T = 96, 256, 12
+    wa, w = make_weights(kind, 4, N, K, 64, 9)
+    (x,), _ = make_x(kind, T, K, 9)
+    dirty = x.clone()
+    dirty[0, 3] = math.nan
+    dirty[5, 0] = math.inf
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    R = sum(counts)
+    rows = (torch.arange(R, device="cuda") % T).to(torch.int32)
+    rows[3], rows[R - 1] = -1, T
+    clean_y = call(wq, kind, (x,), wa, off, rows, 64, False)
+    y = call(wq, kind, (dirty,), wa, off, rows, 64, False)
+    keep = (rows != 0) & (rows != 5)
+    assert torch.equal(y[keep], clean_y[keep])
+    assert torch.isnan(y[rows == 0]).all() and not torch.isfinite(y[rows == 5]).any()
+    assert (y[3] == 0).all() and (y[R - 1] == 0).all()
+    # One infinity: each sum has the sign of its weight, or is NaN where the weight is zero.
+    expert = torch.searchsorted(off.long(), torch.arange(R, device="cuda"), right=True) - 1
+    for p in (rows == 5).nonzero().flatten().tolist():
+        s = torch.sign(w[expert[p], :, 0])
+        assert torch.equal(torch.nan_to_num(torch.sign(y[p].double()), 0.0), s)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("R,K,N", [(20, 512, 136), (20, 512, 2000), (20, 512, 9500), (60, 512, 136), (60, 4096, 136)])
+def test_few_rows_graph_replay_with_new_routing(wq, kind, R, K, N):
+    T, E = 60, 5
+    wa, w = make_weights(kind, E, N, K, 128, 8)
+    xa, x = make_x(kind, T, K, 8)
+    off = torch.tensor([0, 2, 2, 9, 10, R], dtype=torch.int32, device="cuda")
+    rows = torch.randint(0, T, (R,), device="cuda", dtype=torch.int32)
+    out = torch.full((R, N), SENTINEL, dtype=xa[0].dtype, device="cuda")
+    call(wq, kind, xa, wa, off, rows, 128, False, out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(wq, kind, xa, wa, off, rows, 128, False, out)
+    for new in ([0, R, R, R, R, R], [0, 1, 2, 3, 4, 5], [10, 10, 10, 10, 10, 10], [0, 4, 8, 12, 16, R - 1]):
+        off.copy_(torch.tensor(new, dtype=torch.int32))
+        rows.copy_(torch.randint(0, T, (R,), dtype=torch.int32))
+        out.fill_(SENTINEL)
+        graph.replay()
+        y, tol, written = product_ref(kind, x, w, rows, off.cpu(), R, K, False)
+        assert ((out.double() - y).abs() <= tol)[written].all()
+        assert (out[~written] == SENTINEL).all()
+
+
+@gpu
+@pytest.mark.parametrize("counts,N", [(HANDFUL, 70), (HANDFUL, 1250), (HANDFUL, 4757), (FEW, 200)])
+def test_few_rows_on_two_streams(wq, counts, N):
+    """Two calls of one kernel that overlap on the GPU share nothing."""
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    R, cases = int(off[-1]), []
+    for i in range(2):
+        wa, _ = make_weights("fp16", len(counts), N, 2304, 128, i)
+        xa, _ = make_x("fp16", 30, 2304, i)
+        rows = torch.randint(0, 30, (R,), device="cuda", dtype=torch.int32)
+        cases.append((xa, wa, rows, call(wq, "fp16", xa, wa, off, rows, 128, False)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [call(wq, "fp16", xa, wa, off, rows, 128, False, stream=st) for (xa, wa, rows, _), st in zip(cases, streams)]
+        torch.cuda.synchronize()
+        for y, c in zip(got, cases):
+            assert torch.equal(y, c[3])
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+def test_few_rows_waits_that_run_out(wq, kind):
+    """As above, for INT4 experts with 6 to 22 rows."""
+    N, K, counts = 640, 2048, [30, 9, 0, 5]
+    wa, _ = make_weights(kind, 4, N, K, 128, 2)
+    T = sum(counts)
+    xa, _ = make_x(kind, T, K, 2)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    good = call(wq, kind, xa, wa, off, None, 128, False)
+    try:
+        wq.set_wait_limit(1)
+        for _ in range(3):
+            call(wq, kind, xa, wa, off, None, 128, False)
+        assert wq.device_status() in (wq.WQ_OK, wq.WQ_ERR_TIMEOUT)
+    finally:
+        wq.set_wait_limit(0)
+    assert torch.equal(call(wq, kind, xa, wa, off, None, 128, False), good)
+    assert wq.device_status() == 0
+
+
 @gpu
 @pytest.mark.parametrize("kind", FORMATS)
 def test_one_expert_equals_the_dense_product(wq, kind):
