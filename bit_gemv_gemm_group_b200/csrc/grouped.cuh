@@ -248,7 +248,7 @@ int resident_clusters(Kernel kern, int threads, size_t smem, int size) {
 // 4 x 2 x 16 rows is 16 gate rows, their 16 up rows, and so on; otherwise boxes of 16 rows.
 bool encode_weights(CUtensorMap *map, const void *w, uint64_t row_bytes, int width, Args &a, bool swiglu);
 
-// INT4 weights and 6 to 22 rows per expert (grouped_few.cu); `bf16`: type of x and y.
+// INT4 weights and 7 to 22 rows per expert (grouped_few.cu); `bf16`: type of x and y.
 wq_status few_rows_w4(const void *w, Args a, bool bf16, bool swiglu, cudaStream_t st, const char *who);
 
 // INT4 weights and a handful of rows per expert (grouped_stream.cu).

@@ -1,4 +1,4 @@
-// Expert products with INT4 weights for few rows per expert (decode batches, 6 to 22): the same products as
+// Expert products with INT4 weights for few rows per expert (decode batches, 7 to 22): the same products as
 // grouped_gemm.cu's kernel, whose tiles these are, organised around the stream of packed weights.
 //
 //   y[p][n] = sum_j s[n][j] * ( sum_{k in group j} (q[n][k] - z[n][j]) x[rows[p]][k] )

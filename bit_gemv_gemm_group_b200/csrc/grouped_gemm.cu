@@ -648,9 +648,10 @@ wq_status dispatch(const void *w, Args a, bool swiglu, cudaStream_t st, const ch
 }
 
 // INT4 experts with fewer rows than this on average go to grouped_stream.cu, the rest to grouped_few.cu.  Measured on
-// B200 by rows per expert: 8 experts of 28672 x 4096, 4 rows 115 against 152 us, 8 rows 178 against 154 (every
-// ninth row of an expert is another tile); 64 experts of 4096 x 2048, 3 rows 84 against 103 us, 6 rows 113 against 117.
-constexpr long long STREAM_ROWS = 6;
+// B200 by rows per expert: 8 experts of 28672 x 4096, 4 rows 109 against 152 us, 7 rows 148 against 154, 8 rows 160
+// against 154 (every ninth row of an expert is another tile); 8 experts of 4096 x 14336, 6 rows 92 against 91; 64 uneven
+// experts of 4096 x 2048, 6 rows 103 against 117 us, 12 rows 154 against 146.
+constexpr long long STREAM_ROWS = 7;
 
 template <Kind KIND>
 wq_status run(const void *x, const void *w, Args a, bool swiglu, cudaStream_t st, const char *who) {

@@ -393,7 +393,7 @@ def test_fp8_scalar_scales(wq):
         assert ((y.double() - ref).abs() <= tol)[written].all()
 
 
-# INT4 by rows per expert: fewer than 6 on average, and below 22.  N for E experts such that there are tiles enough for
+# INT4 by rows per expert: fewer than 7 on average, and below 22.  N for E experts such that there are tiles enough for
 # each of the shapes that the first of them takes.
 HANDFUL = [1, 8, 0, 9, 3, 2, 17, 1]
 FEW = [9, 0, 40, 7]
@@ -519,7 +519,7 @@ def test_few_rows_on_two_streams(wq, counts, N):
 @gpu
 @pytest.mark.parametrize("kind", ["fp16", "bf16"])
 def test_few_rows_waits_that_run_out(wq, kind):
-    """As above, for INT4 experts with 6 to 22 rows."""
+    """As above, for INT4 experts with 7 to 22 rows."""
     N, K, counts = 640, 2048, [30, 9, 0, 5]
     wa, _ = make_weights(kind, 4, N, K, 128, 2)
     T = sum(counts)
