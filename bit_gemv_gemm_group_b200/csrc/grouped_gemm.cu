@@ -701,6 +701,21 @@ wq_status check_sizes(const char *who, int T, const int32_t *rows, const int32_t
     return WQ_OK;
 }
 
+// y is written while the inputs are read.  `bits`: of a weight.
+wq_status check_output(const char *who, const Args &a, const void *x, int x_bytes, const void *w, int bits, int swiglu) {
+    const size_t y_bytes = (size_t)a.R * (swiglu ? a.N / 2 : a.N) * 2, weights = (size_t)a.E * a.N * a.K;
+    const size_t groups = a.gs ? a.K / a.gs : 0, rows = (size_t)a.E * a.N;
+    const bool bad = overlap(a.y, y_bytes, x, (size_t)a.T * a.K * x_bytes) || overlap(a.y, y_bytes, w, weights * bits / 8) ||
+                     overlap(a.y, y_bytes, a.offsets, ((size_t)a.E + 1) * 4) ||
+                     (a.rows && overlap(a.y, y_bytes, a.rows, (size_t)a.R * 4)) ||
+                     (a.scales && overlap(a.y, y_bytes, a.scales, rows * groups * 2)) ||
+                     (a.qzeros && overlap(a.y, y_bytes, a.qzeros, rows * ((groups + 7) / 8) * 4)) ||
+                     (a.sx && overlap(a.y, y_bytes, a.sx, a.sx_stride ? (size_t)a.T * 4 : 4)) ||
+                     (a.sw && overlap(a.y, y_bytes, a.sw, (a.sw_per_row ? rows : (size_t)a.E) * 4));
+    WQ_REQUIRE(!bad, WQ_ERR_INVALID_ARG, "%s: y overlaps an input", who);
+    return WQ_OK;
+}
+
 template <Kind KIND>
 wq_status w4_entry(const uint16_t *x, int T, const int32_t *rows, const int32_t *offsets, int R,
                    const uint32_t *qweight, const uint16_t *scales, const uint32_t *qzeros, int E, int N, int K,
@@ -723,6 +738,8 @@ wq_status w4_entry(const uint16_t *x, int T, const int32_t *rows, const int32_t 
     a.qzeros = qzeros;
     a.y = y;
     a.T = T; a.R = R; a.E = E; a.N = N; a.K = K; a.gs = group_size;
+    const wq_status o = check_output(who, a, x, 2, qweight, 4, swiglu);
+    if (o != WQ_OK) return o;
     return run<KIND>(x, qweight, a, swiglu != 0, as_stream(stream), who);
 }
 
@@ -749,6 +766,8 @@ wq_status w8_entry(const void *xq, const float *sx, int sx_per_row, int T, const
     a.sw_per_row = sw_per_row != 0;
     a.y = y;
     a.T = T; a.R = R; a.E = E; a.N = N; a.K = K;
+    const wq_status o = check_output(who, a, xq, 1, wq_, 8, swiglu);
+    if (o != WQ_OK) return o;
     return run<KIND>(xq, wq_, a, swiglu != 0, as_stream(stream), who);
 }
 

@@ -329,9 +329,7 @@ wq_status launch(const void *w, Args a, cudaStream_t st, const char *who) {
     WQ_REQUIRE(most < INT_MAX / 2, WQ_ERR_UNSUPPORTED, "%s: R (%d) x N (%d) gives too many tiles", who, a.R, a.N);
     const int grid = (int)std::min<long long>((long long)num_sms() * (SM_WARPS / WARPS), most);
     kern<<<grid, WARPS * 32, L::bytes(a.E), st>>>(static_cast<const uint8_t *>(w), a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return fail(WQ_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
-    return WQ_OK;
+    return check_launch(who);
 }
 
 // Tiles and warps by the number of tiles of 64 weight rows (if every row had an expert of its own): four warps a

@@ -472,6 +472,10 @@ extern "C" wq_status wq_moe_combine(const uint16_t *y, wq_dtype dtype, int R, co
                "wq_moe_combine: sizes must be positive (R=%d T=%d top_k=%d N=%d)", R, T, top_k, N);
     WQ_REQUIRE(dtype == WQ_F16 || dtype == WQ_BF16, WQ_ERR_INVALID_ARG,
                "wq_moe_combine: dtype must be WQ_F16 or WQ_BF16 (got %d)", (int)dtype);
+    const size_t bytes = (size_t)T * N * 2, pairs = (size_t)T * top_k * 4;
+    WQ_REQUIRE(!overlap(out, bytes, y, (size_t)R * N * 2) && !overlap(out, bytes, weights, pairs) &&
+                   !overlap(out, bytes, slots, pairs),
+               WQ_ERR_INVALID_ARG, "wq_moe_combine: out overlaps an input");
     cudaStream_t st = as_stream(stream);
     if (dtype == WQ_BF16) return combine_dispatch<true>(y, R, weights, slots, T, top_k, N, out, st);
     return combine_dispatch<false>(y, R, weights, slots, T, top_k, N, out, st);

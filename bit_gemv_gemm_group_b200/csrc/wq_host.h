@@ -36,6 +36,12 @@ inline wq_status check_launch(const char *what) {
 
 int num_sms();
 
+// Whether two ranges of bytes share any.
+inline bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return p < q + b_bytes && q < p + a_bytes;
+}
+
 // Encodes a 2-D tiled TMA descriptor over a row-major [outer][inner] array
 // (element size `elem_bytes`, row pitch `row_bytes`) with box
 // [box_outer][box_inner].  Returns false and records a message on failure.

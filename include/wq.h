@@ -471,8 +471,8 @@ wq_status wq_moe_route(const void *logits, wq_dtype dtype, int T, int E, int top
  * offsets[E] on are not written.  An entry of rows outside [0, T) gives a row
  * of zeros; offsets outside their range are clamped to it and made
  * non-decreasing, so that no value of either reads or writes out of bounds.
- * A NaN or infinity in a row of x stays in that row of y.  y must not overlap
- * an input.
+ * A NaN or infinity in a row of x stays in that row of y.  A y that overlaps an
+ * input is refused.
  * Rounding of the INT4 weights: with at least 22 rows per expert on average (R
  * against the experts, or R, whichever are fewer) each s (q - z) is rounded to
  * the type of x, as in wq_gemm_w4a16; below, it is not: the codes are
@@ -499,7 +499,8 @@ wq_status wq_grouped_gemm_fp8(const uint8_t *xq, const float *sx, int sx_per_row
  * in fp32 in the order of j; a slot outside [0, R) (a choice without an
  * expert) adds nothing, so a token without any gives zeros.
  * y: [R][N] and out: [T][N] of dtype WQ_F16 or WQ_BF16;  weights: fp32
- * [T][top_k];  slots: int32 [T][top_k].  out must not overlap y.
+ * [T][top_k];  slots: int32 [T][top_k].  An out that overlaps an
+ * input is refused.
  */
 wq_status wq_moe_combine(const uint16_t *y, wq_dtype dtype, int R, const float *weights, const int32_t *slots, int T,
                          int top_k, int N, uint16_t *out, void *stream);

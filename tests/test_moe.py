@@ -100,6 +100,31 @@ def test_combine_refusals(wq):
     assert call(R=0) == inv and call(T=0) == inv and call(k=0) == inv and call(N=0) == inv
 
 
+def test_outputs_that_overlap_inputs_are_refused(wq):
+    """The sizes are known, so an output inside, across the start or across the end of an input is an error."""
+    at = lambda o: ctypes.c_void_p(0x1000000 + o)  # noqa: E731
+    far = [ctypes.c_void_p((i + 2) << 32) for i in range(8)]
+    inv = wq.WQ_ERR_INVALID_ARG
+    T, R, E, N, K = 4, 8, 2, 64, 256
+    x4, w4, x8, w8, out = T * K * 2, E * N * K // 2, T * K, E * N * K, R * N * 2
+    for sizes, call in (
+            ((x4, 32, 12, w4, E * N * 4, E * N * 4), lambda y, p: wq.lib.wq_grouped_gemm_w4a16(
+                p[0], T, p[1], p[2], R, p[3], p[4], p[5], E, N, K, 128, 0, y, None)),
+            ((x8, 32, 12, w8, T * 4, E * N * 4), lambda y, p: wq.lib.wq_grouped_gemm_w8a8(
+                p[0], p[4], T, p[1], p[2], R, p[3], p[5], E, N, K, 0, y, None)),
+            ((x8, 32, 12, w8, 4, E * 4), lambda y, p: wq.lib.wq_grouped_gemm_fp8(
+                p[0], p[4], 0, T, p[1], p[2], R, p[3], p[5], 0, E, N, K, 0, y, None)),
+            ((R * N * 2, T * 2 * 4, T * 2 * 4), lambda y, p: wq.lib.wq_moe_combine(p[0], 1, R, p[1], p[2], T, 2, N, y, None))):
+        for i, size in enumerate(sizes):
+            p = list(far)
+            p[i] = at(0)
+            last = (size - 1) // 16 * 16
+            y_bytes = out if len(sizes) == 6 else T * N * 2
+            for o in (0, last, 16 - y_bytes):
+                assert call(at(o), p) == inv, (i, o)
+                assert b"overlaps" in wq.lib.wq_last_error()
+
+
 # ------------------------------------------------------------------------------------------------ router
 def route_ref(logits, k, renorm):
     x = logits.double().cpu().numpy()
