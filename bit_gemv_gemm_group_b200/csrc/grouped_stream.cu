@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(WARPS * 32, SM_WARPS / WARPS)
         up = gate + (size_t)(a.N / 2) * pitch;
         last = min(BN, a.ldy - nw.n0) - 1 - r;
         whole = last + r == BN - 1;
-        // Past the tile's rows and for an index outside x: row 0, whose sums are not stored.
+        // Past the tile's rows the last of them, for an index outside x row 0: their sums are not stored.
         int v = nw.r0 + min(r, nw.rows - 1);
         if (a.rows) v = __ldg(a.rows + v);
         xp = a.x + ((unsigned)v < (unsigned)a.T ? (size_t)v : 0) * ((size_t)a.K * 2) + (SUB == 1 ? t * 64 : t * 16);
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(WARPS * 32, SM_WARPS / WARPS)
 #pragma unroll
         for (int u = 0; u < CPL; ++u) {
 #pragma unroll
-            for (int s = 0; s < SUB; ++s) ns[u][s] = load16(srow[u] + (ALL ? g0 + s : min(g0 + s, groups - 1)));
+            for (int s = 0; s < SUB; ++s) ns[u][s] = ALL || g0 + s < groups ? load16(srow[u] + g0 + s) : 0u;
             nz[u] = load32(zrow[u] + (g0 >> 3)) >> (4 * (g0 & 7));
         }
     };

@@ -498,6 +498,29 @@ def test_nan_and_inf_beside_few_rows(wq, kind, counts):
 
 @gpu
 @pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("counts", [[2, 1], [12, 9]])
+@pytest.mark.parametrize("group,K", [(32, 160), (64, 192), (128, 384)])
+def test_infinite_scales_beside_the_end_of_few_rows(wq, kind, counts, group, K):
+    """The last group's scale is infinite: sums get its sign, also where the depth ends inside a step of the kernel."""
+    N, T = 40, sum(counts)
+    (q, s, z), _ = make_weights(kind, 2, N, K, group, 4)
+    (x,), x64 = make_x(kind, T, K, 4)
+    s = s.clone()
+    s[:, ::2, -1] = math.inf
+    off = torch.tensor([0, counts[0], T], dtype=torch.int32, device="cuda")
+    y = wq.grouped_gemm_w4a16(x, q, s, z, off, group_size=group)
+    nibbles = torch.arange(0, 32, 4, device="cuda", dtype=torch.int32)
+    codes = ((q.unsqueeze(-1) >> nibbles) & 15).view(2, N, K).double()
+    zeros = ((z.unsqueeze(-1) >> nibbles) & 15).view(2, N, -1)[..., :K // group].double()
+    last = codes[..., -group:] - zeros[..., -1:]
+    for p in range(T):
+        d = last[0 if p < counts[0] else 1] @ x64[p, -group:]
+        assert torch.equal(y[p, ::2].double(), torch.sign(d[::2]) * math.inf)
+        assert torch.isfinite(y[p, 1::2]).all()
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
 @pytest.mark.parametrize("R,K,N", [(20, 512, 136), (20, 512, 2000), (20, 512, 9500), (60, 512, 136), (60, 4096, 136)])
 def test_few_rows_graph_replay_with_new_routing(wq, kind, R, K, N):
     T, E = 60, 5
@@ -696,6 +719,48 @@ def test_output_past_32_bit_offsets(wq):
     for p, e in ((0, 0), (70000, 0), (70001, 1), (131071, 1), (139989, 1), (139990, 2), (R - 1, 2)):
         ref = (xq[p].double() * sx[p].double()) @ w[e].T
         assert ((y[p].double() - ref).abs() <= ref.abs() * (2.0 ** -11 + 2.0 ** -22) + 2.0 ** -25).all()
+
+
+@gpu
+@pytest.mark.parametrize("R", [2, 300, 900])
+def test_int4_weights_past_32_bit_offsets(wq, R):
+    """4.7 GB of codes: the last expert's rows, by each of the INT4 kernels (below 7, below 22 and more rows per expert)."""
+    E, N, K, group = 40, 28672, 8192, 128
+    g = torch.Generator(device="cuda").manual_seed(R)
+    q = torch.randint(-2 ** 31, 2 ** 31, (E, N, K // 8), device="cuda", dtype=torch.int32, generator=g)
+    s = torch.full((E, N, K // group), 2.0 ** -6, dtype=torch.float16, device="cuda")
+    s[-1] = (torch.rand(N, K // group, device="cuda", generator=g) * 2.0 ** -6).half()
+    z = torch.randint(-2 ** 31, 2 ** 31, (E, N, K // group // 8), device="cuda", dtype=torch.int32, generator=g)
+    x = torch.randn(R, K, device="cuda", generator=g).half()
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[-1] = R
+    y = wq.grouped_gemm_w4a16(x, q, s, z, off, group_size=group)
+    at = torch.tensor([0, 1, 63, 64, 14335, 28671], device="cuda")
+    nibbles = torch.arange(0, 32, 4, device="cuda", dtype=torch.int32)
+    codes = ((q[-1, at].unsqueeze(-1) >> nibbles) & 15).view(len(at), K).double()
+    zeros = ((z[-1, at].unsqueeze(-1) >> nibbles) & 15).view(len(at), -1).double()
+    w = (codes - zeros.repeat_interleave(group, 1)) * s[-1, at].double().repeat_interleave(group, 1)
+    ref, size = x.double() @ w.T, x.double().abs() @ w.abs().T
+    u = 2.0 ** -11
+    tol = (u + K * 2.0 ** -23) * size + 2.0 ** -25 * x.double().abs().sum(1, keepdim=True)
+    assert ((y[:, at].double() - ref).abs() <= tol + (ref.abs() + tol) * u + 2.0 ** -25).all()
+
+
+@gpu
+@pytest.mark.parametrize("R", [5, 900])
+def test_int8_weights_past_32_bit_offsets(wq, R):
+    E, N, K = 20, 28672, 8192
+    g = torch.Generator(device="cuda").manual_seed(R)
+    q = torch.randint(-128, 128, (E, N, K), device="cuda", dtype=torch.int8, generator=g)
+    sw = torch.rand(E, N, device="cuda", generator=g) * 2.0 ** -10
+    x = torch.randint(-128, 128, (R, K), device="cuda", dtype=torch.int8, generator=g)
+    sx = torch.full((R,), 2.0 ** -6, device="cuda")
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[-1] = R
+    y = wq.grouped_gemm_w8a8(x, sx, q, sw, off)
+    at = torch.tensor([0, 127, 128, 28671], device="cuda")
+    ref = (x.double() @ q[-1, at].double().T) * 2.0 ** -6 * sw[-1, at].double()
+    assert ((y[:, at].double() - ref).abs() <= ref.abs() * (2.0 ** -11 + 2.0 ** -22) + 2.0 ** -25).all()
 
 
 @gpu
