@@ -451,8 +451,8 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
     } else if (GATHER && warp >= L::GA_WARP0 && warp < L::GA_WARP0 + GATHER_WARPS) {
         // -------------------------------------------------------------------- gathered activations
         // Thread (16-byte chunk c of a row's 128 bytes, row rr of every 16): cp.async into the 128-byte
-        // swizzle, whose completion arrives on the stage's barrier by itself.  Padding repeats the last row; an index outside x reads row 0 (the
-        // epilogue writes zeros for it).
+        // swizzle, whose completion arrives on the stage's barrier by itself.  Padding repeats the last row; an
+        // index outside x reads row 0 (the epilogue writes zeros for it).
         constexpr int PASSES = L::SR / 16;
         const int gt = (int)threadIdx.x - 32 * L::GA_WARP0, c = gt & 7, rr = gt >> 3;
         const size_t pitch = (size_t)a.K * (W4 ? 2 : 1);
