@@ -573,25 +573,25 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, worksp
     T, E = logits.shape
     k = int(top_k)
     cols = max(k, 0)
-    n = (T * cols + 3) & ~3                    # one allocation, every part 16-byte aligned
-    new = logits.new_empty
-    buf = new((4 * n + E + 1,), dtype=torch.int32)
+    need = lib.wq_moe_route_workspace_bytes(T, E)
+    n = (T * cols + 3) & ~3                    # one allocation, every part 16-byte aligned; the workspace comes last
+    end = 4 * n + ((E + 4) & ~3)
+    buf = logits.new_empty((end + (need + 3) // 4 if workspace is None else end,), dtype=torch.int32)
     ids = buf.as_strided((T, cols), (cols, 1), 0)
     weights = buf.view(torch.float32).as_strided((T, cols), (cols, 1), n)
     slots = buf.as_strided((T, cols), (cols, 1), 2 * n)
     rows = buf.as_strided((T * cols,), (1,), 3 * n)
     offsets = buf.as_strided((E + 1,), (1,), 4 * n)
-    need = lib.wq_moe_route_workspace_bytes(T, E)
     if workspace is None:
-        workspace = new((need,), dtype=torch.uint8) if need else None
+        scratch = buf.data_ptr() + 4 * end
     else:
         _cuda(workspace, "workspace", (torch.uint8,), 1)
         if workspace.numel() < need or workspace.device != logits.device:
             raise ValueError(f"workspace must hold {need} bytes on {logits.device}")
+        scratch = workspace.data_ptr()
     status = lib.wq_moe_route(logits.data_ptr(), _DTYPE[logits.dtype], T, E, k, 1 if renormalize else 0,
                               ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
-                              slots.data_ptr(), None if workspace is None else workspace.data_ptr(),
-                              _moe_stream(logits, None))
+                              slots.data_ptr(), scratch, _moe_stream(logits, None))
     if status:
         _check(status, "wq_moe_route")
     return ids, weights, offsets, rows, slots

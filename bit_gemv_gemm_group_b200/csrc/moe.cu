@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(THREADS) route_place_kernel(RouteArgs a) {
         mark(bits, ids, pairs, a.k);
         __syncthreads();
         place(bits, base, ids, a, t, pairs);
+        if (t + CHUNK >= t1) break;
         __syncthreads();
         for (int e = threadIdx.x; e < E; e += THREADS) {
             base[e] += set_bits(bits, e);
