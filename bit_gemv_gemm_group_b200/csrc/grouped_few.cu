@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ep ^= 1;
             }
         }
+        tmem_st_wait();   // after a wait that ran out, stores of half a pack may still be in flight
     }
 
     tc_fence_before();

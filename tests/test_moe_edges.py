@@ -1,0 +1,38 @@
+"""Mixture-of-experts operators at their edges: calls that give up, depths and scales that end inside a tile, far values,
+arguments that do not fit together.  The references and tolerances are those of test_moe.py unless a test derives its own.
+"""
+import numpy as np
+import pytest
+import torch
+
+from test_moe import call, make_weights, make_x, wq  # noqa: F401  (wq: the fixture)
+
+gpu = pytest.mark.gpu
+
+
+def offsets(counts):
+    return torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------------------------------------ expired waits
+@gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+def test_few_rows_under_a_tiny_limit_leave_the_device_as_it_was(wq, kind):
+    """7 to 22 rows per INT4 expert, a CTA per tile: calls whose waits may run out while half a pack's stores to tensor
+    memory are under way end, and the next calls give the results of the first."""
+    N, K, counts = 9472, 8192, [16]
+    wa, _ = make_weights(kind, 1, N, K, 128, 2)
+    xa, _ = make_x(kind, sum(counts), K, 2)
+    off = offsets(counts)
+    good = call(wq, kind, xa, wa, off, None, 128, False)
+    assert wq.device_status() == 0
+    try:
+        wq.set_wait_limit(1)
+        for _ in range(5):
+            call(wq, kind, xa, wa, off, None, 128, False)
+        assert wq.device_status() in (wq.WQ_OK, wq.WQ_ERR_TIMEOUT)
+    finally:
+        wq.set_wait_limit(0)
+    for _ in range(3):
+        assert torch.equal(call(wq, kind, xa, wa, off, None, 128, False), good)
+    assert wq.device_status() == 0
