@@ -319,19 +319,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // and loads are contiguous.
                 if (rank != 0) {
                     if (n > 0) {
-                        ok = wait_parity_lean(smem_u32(&bar->red_free[q]), (n - 1) & 1, ctl, SITE_SPLIT);
+                        ok = wait_parity_lean<true>(smem_u32(&bar->red_free[q]), (n - 1) & 1, ctl, SITE_SPLIT);
                         if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                        fence_cluster();
                     }
                     const uint32_t dst = mapa_shared(sR + (rank - 1) * RED_BYTES + trow * 4, 0);
 #pragma unroll
                     for (int j = 0; j < BR; ++j)
                         st_cluster_f32(dst + j * BM * 4, acc[j]);
-                    fence_cluster();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bar->red_full[q]), 0));
+                    if (lane == 0) {   // releases the whole warp's stores
+                        fence_cluster();
+                        mbar_arrive_cluster(mapa_shared(smem_u32(&bar->red_full[q]), 0));
+                    }
                     continue;
                 }
-                ok = wait_parity_lean(smem_u32(&bar->red_full[q]), n & 1, ctl, SITE_SPLIT);
+                ok = wait_parity_lean<true>(smem_u32(&bar->red_full[q]), n & 1, ctl, SITE_SPLIT);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 fence_cluster();
                 for (int c = 0; c < split - 1; ++c) {
@@ -341,7 +344,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         acc[j] += part[j * BM];
                 }
                 __syncwarp();
-                if (lane > 0 && lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(&bar->red_free[q]), lane));
+                if (lane > 0 && lane < split) {
+                    fence_cluster();
+                    mbar_arrive_cluster(mapa_shared(smem_u32(&bar->red_free[q]), lane));
+                }
             }
             const int col = cur.n0 + (SWIGLU ? 16 * q + (lane & 15) : 32 * q + lane);
             const bool col_ok = col < a.ldy;

@@ -21,9 +21,8 @@
 //
 // Persistent warp-specialized CTA, one per SM:
 //   warp 0      TMA: weight tiles (8-bit kinds) and, when the rows lie in order, activations
-//   warp 1      an elected thread issues tcgen05.mma into one of two accumulators; in the pair's second CTA it
-//               passes on to the first that a stage is filled
-//   warp 2      allocates tensor memory
+//   warp 1      an elected thread issues tcgen05.mma into one of two accumulators
+//   warp 2      allocates tensor memory; in the pair's second CTA it and warp 1 tell the first that a stage is filled
 //   warp 3      (INT4) packed weight tiles, 128 rows x 64 bytes (two stages), into a ring of their own
 //   warps 4-7   epilogue of the previous tile: scales, SwiGLU, conversion, stores (4-11 for 8-bit pairs)
 //   then        four warps that gather indexed activation rows by cp.async (TMA's gather of four rows a
@@ -285,37 +284,59 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
             }
         }
         __syncwarp();
+    } else if (PAIR && rank == 1 && (warp == 1 || warp == 2)) {
+        // -------------------------------------------------------------------- the second CTA's stages are filled
+        // Each warp tells the first CTA of every other stage, so that the fence of one overlaps the other's wait.
+        const bool leader = elect_one();
+        uint32_t it = warp - 1, end = 0;
+        bool ok = true;
+        for (int t = first; ok && get_tile<BN, BR, STEP>(a, off, tiles, t, w); t += stride) {
+            for (end += kst; it < end; it += 2) {
+                const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
+                const uint32_t fb = smem_u32(&bar->full[s]), pb = smem_u32(&bar->put[s]);
+                if (GATHER || W4)
+                    ok = TMA_STAGE ? wait_parity2(fb, ph, pb, ph, ctl, SITE_MMA) : wait_parity_lean(pb, ph, ctl, SITE_MMA);
+                else
+                    ok = wait_parity_lean(fb, ph, ctl, SITE_MMA);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+                if (GATHER) fence_proxy_async_smem();  // rows copied by cp.async, read by the tensor cores
+                if (leader) {
+                    fence_release_smem();
+                    mbar_arrive_cluster(mapa_shared(pb, 0));
+                }
+                __syncwarp();
+            }
+        }
     } else if (warp == 1) {
         // -------------------------------------------------------------------- MMA issuer
         const bool leader = elect_one();
-        constexpr bool PUT0 = GATHER || W4 || PAIR, PUT1 = GATHER || W4;  // `put` is used in rank 0 / rank 1
         const uint64_t desc_a = umma_desc_sw128_kmajor(sA), desc_b = umma_desc_sw128_kmajor(sB);
         uint32_t s = 0, ph = 0, n = 0;
         bool ok = true;
         for (int t = first; ok && get_tile<BN, BR, STEP>(a, off, tiles, t, w); t += stride, ++n) {
             const uint32_t acc = n & 1, d = tmem_base + acc * BR;
             const uint32_t idesc = idesc_rows<KIND>(PAIR ? 2 * BM : BM, local_rows(w) * (PAIR ? 2 : 1));
-            if (rank == 0) {
-                ok = wait_parity_lean(smem_u32(&bar->acc_empty[acc]), ((n >> 1) & 1) ^ 1, ctl, SITE_MMA);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            }
+            const uint32_t ae = smem_u32(&bar->acc_empty[acc]), ap = ((n >> 1) & 1) ^ 1;
+            ok = PAIR ? wait_parity_cluster(ae, ap, ctl, SITE_MMA) : wait_parity_lean(ae, ap, ctl, SITE_MMA);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
             for (int kb = 0; kb < kst; ++kb) {
-                ok = (!TMA_STAGE || wait_parity_lean(smem_u32(&bar->full[s]), ph, ctl, SITE_MMA)) &&
-                     (!(rank == 0 ? PUT0 : PUT1) || wait_parity_lean(smem_u32(&bar->put[s]), ph, ctl, SITE_MMA));
+                const uint32_t fb = smem_u32(&bar->full[s]), pb = smem_u32(&bar->put[s]);
+                if (PAIR)
+                    ok = TMA_STAGE ? wait_parity_cluster(pb, ph, fb, ctl, SITE_MMA)
+                                   : wait_parity_cluster(pb, ph, ctl, SITE_MMA);
+                else
+                    ok = GATHER ? wait_parity2(fb, ph, pb, ph, ctl, SITE_MMA) : wait_parity_lean(fb, ph, ctl, SITE_MMA);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
                 if (GATHER) fence_proxy_async_smem();  // rows copied by cp.async, read by the tensor cores
                 if (leader) {
-                    if (rank == 0) {
-                        const uint64_t da = desc_a + s * (A_BYTES >> 4), db = desc_b + s * (L::B_BYTES >> 4);
+                    const uint64_t da = desc_a + s * (A_BYTES >> 4), db = desc_b + s * (L::B_BYTES >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < STAGE_K / 32; ++kk)
-                            mma_step<KIND, PAIR>(d, da + 2 * kk, db + 2 * kk, idesc, kb != 0 || kk != 0);
-                        if (PAIR) tc_commit_pair_both(smem_u32(&bar->empty[s]));
-                        else tc_commit(smem_u32(&bar->empty[s]));
-                    } else {
-                        mbar_arrive_cluster(mapa_shared(smem_u32(&bar->put[s]), 0));
-                    }
+                    for (int kk = 0; kk < STAGE_K / 32; ++kk)
+                        mma_step<KIND, PAIR>(d, da + 2 * kk, db + 2 * kk, idesc, kb != 0 || kk != 0);
+                    if (PAIR) tc_commit_pair_both(smem_u32(&bar->empty[s]));
+                    else tc_commit(smem_u32(&bar->empty[s]));
                 }
                 __syncwarp();
                 if (++s == STAGES) {
@@ -323,13 +344,13 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                     ph ^= 1;
                 }
             }
-            if (ok && leader && rank == 0) {
+            if (ok && leader) {
                 if (PAIR) tc_commit_pair_both(smem_u32(&bar->acc_full[acc]));
                 else tc_commit(smem_u32(&bar->acc_full[acc]));
             }
             __syncwarp();
         }
-        if (leader && rank == 0) {
+        if (leader) {
             if (PAIR) tc_commit_pair(smem_u32(&bar->drain));
             else tc_commit(smem_u32(&bar->drain));
             drain_parity(smem_u32(&bar->drain), 0, DRAIN_NS, a.status, SITE_DRAIN);
@@ -444,8 +465,12 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&bar->acc_empty[acc]), 0));
-                else mbar_arrive(smem_u32(&bar->acc_empty[acc]));
+                if (PAIR) {
+                    fence_release_smem();
+                    mbar_arrive_cluster(mapa_shared(smem_u32(&bar->acc_empty[acc]), 0));
+                } else {
+                    mbar_arrive(smem_u32(&bar->acc_empty[acc]));
+                }
             }
         }
     } else if (GATHER && warp >= L::GA_WARP0 && warp < L::GA_WARP0 + GATHER_WARPS) {

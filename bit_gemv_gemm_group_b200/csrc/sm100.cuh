@@ -105,15 +105,35 @@ __device__ __forceinline__ bool wait_parity(uint32_t bar, uint32_t parity, const
     }
 }
 
+// The same test for a barrier that another CTA of the cluster arrives on.  It orders nothing by itself.
+__device__ __forceinline__ bool mbar_try_wait_relaxed(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Orders what other CTAs of the cluster released of their shared memory before this thread's next accesses.
+__device__ __forceinline__ void fence_acquire_smem() {
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
+
 // wait_parity for kernels whose other warps need the issue slots: the abort flag and the clock, about 20
-// instructions, are looked at after every 16th test only.
+// instructions, are looked at after every 16th test only.  RELAXED: the test is mbar_try_wait_relaxed.
+template <bool RELAXED = false>
 __device__ __forceinline__ bool wait_parity_lean(uint32_t bar, uint32_t parity, const WaitCtl &c, unsigned site) {
-    if (mbar_try_wait(bar, parity)) return true;
+    auto test = [&] { return RELAXED ? mbar_try_wait_relaxed(bar, parity) : mbar_try_wait(bar, parity); };
+    if (test()) return true;
     const uint64_t t0 = globaltimer();
     while (true) {
 #pragma unroll 1
         for (int i = 0; i < 16; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
+            if (test()) return true;
         if (*c.abort) return false;
         if (globaltimer() - t0 > c.limit_ns) {
             *c.abort = 1;
@@ -121,6 +141,23 @@ __device__ __forceinline__ bool wait_parity_lean(uint32_t bar, uint32_t parity, 
             return false;
         }
     }
+}
+
+// Waits on a barrier that another CTA of the cluster arrives on: what that CTA released of its shared memory before it
+// arrived happens before what this thread does next.
+__device__ __forceinline__ bool wait_parity_cluster(uint32_t bar, uint32_t parity, const WaitCtl &c, unsigned site) {
+    const bool ok = wait_parity_lean<true>(bar, parity, c, site);
+    fence_acquire_smem();
+    return ok;
+}
+
+// The same, and the same phase of a barrier of this CTA's own; both are tested at once (see wait_parity2).
+__device__ __forceinline__ bool wait_parity_cluster(uint32_t bar, uint32_t parity, uint32_t own, const WaitCtl &c,
+                                                    unsigned site) {
+    const bool b0 = mbar_try_wait_relaxed(bar, parity), b1 = mbar_try_wait(own, parity);
+    const bool ok = (b0 || wait_parity_lean<true>(bar, parity, c, site)) && (b1 || wait_parity_lean(own, parity, c, site));
+    fence_acquire_smem();
+    return ok;
 }
 
 // Waits for a phase of each of two barriers, testing both at once: a test takes about 100 cycles to answer.
@@ -374,19 +411,24 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// Orders this thread's accesses to the cluster's shared memory around a barrier of mbar_arrive_cluster.
+// Release and acquire of cluster scope around the barriers that another CTA arrives on.  The first orders every access;
+// the other two only those to this CTA's own shared memory (release) and to the cluster's (acquire), which is all that
+// the CTAs of a pair hand over: ordering every access took them 0.5 us a stage.
 __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
+__device__ __forceinline__ void fence_release_smem() {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
 
 // Full cluster barrier; every thread of every CTA in the cluster takes part.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// Arrives on a barrier of any CTA of the cluster (address from mapa_shared).  The arrival carries no
-// cluster-scope fence (one took most of a microsecond per arrival): it reports shared memory of this CTA,
-// which the tensor core of this SM reads, or tensor memory that has been read, never global data.
+// Arrives on a barrier of any CTA of the cluster (address from mapa_shared) and orders nothing by itself: a release
+// fence of cluster scope comes before it, and the other side waits by wait_parity_cluster.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 // ---------------------------------------------------------------- CTA pairs

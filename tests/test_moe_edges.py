@@ -36,3 +36,31 @@ def test_few_rows_under_a_tiny_limit_leave_the_device_as_it_was(wq, kind):
     for _ in range(3):
         assert torch.equal(call(wq, kind, xa, wa, off, None, 128, False), good)
     assert wq.device_status() == 0
+
+
+# ------------------------------------------------------------------------------------------------ CTAs that share a tile
+@gpu
+@pytest.mark.parametrize("kind,counts,N,K,group", [
+    ("w8a8", [300, 0, 129, 70], 700, 4112, 32), ("fp8", [300, 0, 129, 70], 700, 4112, 32),
+    ("fp16", [300, 0, 129, 70], 700, 4160, 32), ("bf16", [300, 0, 129, 70], 700, 4160, 32),       # pairs
+    ("fp16", [20, 9, 0, 14], 200, 4160, 32), ("bf16", [20, 9, 0, 14], 200, 4224, 128)])           # a depth that is shared
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_shared_tiles_always_give_the_same(wq, kind, counts, N, K, group, swiglu):
+    """What one CTA of a cluster hands to another arrives whole: the same call gives the same bits every time, beside
+    other work on the device too."""
+    wa, _ = make_weights(kind, len(counts), N, K, group, 11)
+    xa, _ = make_x(kind, 50, K, 11)
+    off = offsets(counts)
+    R = sum(counts)
+    rows = torch.randint(0, 50, (R,), device="cuda", dtype=torch.int32)
+    in_order = tuple(t[rows.long()].contiguous() for t in xa)
+    good = call(wq, kind, xa, wa, off, rows, group, swiglu)
+    other, noise = torch.cuda.Stream(), torch.empty(1 << 26, device="cuda")
+    for i in range(60):
+        if i % 3 == 0:
+            with torch.cuda.stream(other):
+                noise.mul_(1.5)
+        assert torch.equal(call(wq, kind, xa, wa, off, rows, group, swiglu), good)
+        assert torch.equal(call(wq, kind, in_order, wa, off, None, group, swiglu), good)
+    torch.cuda.synchronize()
+    assert wq.device_status() == 0
