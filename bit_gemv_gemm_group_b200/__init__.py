@@ -555,7 +555,15 @@ def _with(first: torch.Tensor, t: torch.Tensor, name: str, dtype, shape) -> None
     raise ValueError(f"{name} is on {t.device}, expected {first.device}")
 
 
+def _int32(**sizes: int) -> None:
+    """Refuses what the C entry points' ints would not hold."""
+    for name, v in sizes.items():
+        if not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{name} ({v}) does not fit 32 bits")
+
+
 def moe_route_workspace_bytes(T: int, E: int) -> int:
+    _int32(T=T, E=E)
     return int(lib.wq_moe_route_workspace_bytes(int(T), int(E)))
 
 
@@ -566,13 +574,15 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, worksp
     logits [T, E] fp32, fp16 or bf16 -> (ids int32 [T, k], weights fp32 [T, k], offsets int32 [E + 1],
     rows int32 [T * k], slots int32 [T, k]).  Equal logits go to the lowest expert; NaN and -inf are never chosen
     (id -1, weight 0, slot -1 where nothing is left).  Expert e's sorted rows are offsets[e]:offsets[e + 1]."""
+    k = int(top_k)
+    _int32(top_k=k)
     _cuda(logits, "logits", (torch.float32, torch.float16, torch.bfloat16), 2)
     if _elsewhere(logits, stream):
         with _enter(logits, stream):
             return moe_route(logits, top_k, renormalize, workspace)
     T, E = logits.shape
-    k = int(top_k)
-    cols = max(k, 0)
+    _int32(T=T, E=E)
+    cols = k if 0 < k <= E else 0              # any other is refused by the call
     need = lib.wq_moe_route_workspace_bytes(T, E)
     n = (T * cols + 3) & ~3                    # one allocation, every part 16-byte aligned; the workspace comes last
     end = 4 * n + ((E + 4) & ~3)
@@ -604,6 +614,7 @@ def _grouped(x, offsets, rows, E, N, swiglu, out, dtype):
     if rows is not None:
         R = rows.numel()
         _with(x, rows, "rows", torch.int32, (R,))
+    _int32(T=T, R=R, N=N, K=x.shape[1])
     if swiglu and N % 2:
         raise ValueError("the weights must have an even number of rows with swiglu")
     cols = N // 2 if swiglu else N
@@ -701,6 +712,7 @@ def moe_combine(y, weights, slots, out=None, stream=None):
     _cuda(slots, "slots", (torch.int32,), 2)
     T, k = slots.shape
     R, N = y.shape
+    _int32(T=T, top_k=k, R=R, N=N)
     _with(y, slots, "slots", torch.int32, (T, k))
     _with(y, weights, "weights", torch.float32, (T, k))
     if out is None:

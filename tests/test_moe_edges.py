@@ -64,3 +64,37 @@ def test_shared_tiles_always_give_the_same(wq, kind, counts, N, K, group, swiglu
         assert torch.equal(call(wq, kind, in_order, wa, off, None, group, swiglu), good)
     torch.cuda.synchronize()
     assert wq.device_status() == 0
+
+
+# ------------------------------------------------------------------------------------------------ arguments
+@pytest.mark.parametrize("top_k", [2 - 2 ** 32, 2 ** 32 + 2, 2 ** 31, -2 ** 31 - 1, 2 ** 64 + 2])
+def test_a_top_k_past_32_bits_is_refused(wq, top_k):
+    """It would reach the C entry point as another number, one that the outputs have no room for."""
+    with pytest.raises(ValueError, match="top_k"):
+        wq.moe_route(torch.zeros(4, 8), top_k)
+    with pytest.raises(ValueError, match="32 bits"):
+        wq.moe_route_workspace_bytes(top_k, 8)
+
+
+@gpu
+def test_a_top_k_that_the_router_does_not_take(wq):
+    logits = torch.zeros(4, 8, device="cuda")
+    for top_k in (0, -1, 9, 2 ** 31 - 1, -2 ** 31):
+        with pytest.raises(wq.WQError):
+            wq.moe_route(logits, top_k)
+
+
+@gpu
+def test_sizes_past_32_bits_are_refused(wq):
+    """A size of 2^32 + n would arrive as n, and all but n rows of the result stay as they were."""
+    many = 2 ** 32 + 32
+    with pytest.raises(ValueError, match="32 bits"):
+        wq.moe_combine(torch.empty(many, 1, dtype=torch.float16, device="cuda"), torch.ones(1, 1, device="cuda"),
+                       torch.zeros(1, 1, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="32 bits"):
+        wq.moe_route(torch.empty(many, 1, dtype=torch.float16, device="cuda"), 1)
+    rows = torch.empty(many, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="32 bits"):
+        wq.grouped_gemm_w8a8(torch.empty(4, 16, dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda"),
+                             torch.empty(1, 2, 16, dtype=torch.int8, device="cuda"), torch.ones(1, 2, device="cuda"),
+                             torch.zeros(2, dtype=torch.int32, device="cuda"), rows)
