@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = PAIR ? (int)cluster_ctarank() : 0;
     const int first = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x, stride = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
-    // Stages of a tile.  INT4: whole packed tiles; past the depth codes and activations are zeros.
+    // Stages of a tile.  INT4: whole packed tiles; past the depth codes, scales and activations are zeros.
     const int packs = (a.K + PK * KE - 1) / (PK * KE), kst = W4 ? packs * PK : (a.K + KE - 1) / KE;
 
     if (threadIdx.x == 0) {
@@ -579,7 +579,10 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                     if (h == 0 || (h << 5 & (a.gs - 1)) == 0) {
                         const int g = min((k0 + 32 * h) >> lg, groups - 1), i = g - min(k0 >> lg, groups - 1);
                         const uint32_t s2 = i < 2 ? cs.x : cs.y;
-                        gc.set((i & 1) ? s2 >> 16 : s2 & 0xFFFFu, (cz >> (4 * (g & 7))) & 0xFu);
+                        // Past the depth weights are zero: codes (0 there) minus a zero point, times a large scale, would be
+                        // infinities that the zeros of x turn into NaN.
+                        const uint32_t s16 = (i & 1) ? s2 >> 16 : s2 & 0xFFFFu;
+                        gc.set(k0 + 32 * h < a.K ? s16 : 0u, (cz >> (4 * (g & 7))) & 0xFu);
                     }
                     if (h == 2) {
                         ok = wait_parity_lean(eb + 8, ph ^ 1, ctl, SITE_DEQUANT);

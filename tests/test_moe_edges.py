@@ -1,11 +1,13 @@
 """Mixture-of-experts operators at their edges: calls that give up, depths and scales that end inside a tile, far values,
 arguments that do not fit together.  The references and tolerances are those of test_moe.py unless a test derives its own.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
 
-from test_moe import call, make_weights, make_x, wq  # noqa: F401  (wq: the fixture)
+from test_moe import call, make_weights, make_x, product_ref, wq  # noqa: F401  (wq: the fixture)
 
 gpu = pytest.mark.gpu
 
@@ -98,3 +100,40 @@ def test_sizes_past_32_bits_are_refused(wq):
         wq.grouped_gemm_w8a8(torch.empty(4, 16, dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda"),
                              torch.empty(1, 2, 16, dtype=torch.int8, device="cuda"), torch.ones(1, 2, device="cuda"),
                              torch.zeros(2, dtype=torch.int32, device="cuda"), rows)
+
+
+# ------------------------------------------------------------------------------------------------ depth and scales
+def pack(codes):
+    """[..., n] 4-bit codes -> int32 words of eight, lowest bits first."""
+    c = torch.nn.functional.pad(codes, (0, -codes.shape[-1] % 8)).unflatten(-1, (-1, 8)).long()
+    v = (c << torch.arange(0, 32, 4, device="cuda")).sum(-1)
+    return torch.where(v >= 2 ** 31, v - 2 ** 32, v).to(torch.int32)
+
+
+INT4_COUNTS = [[2, 1], [12, 9], [70, 50], [300, 41]]    # below 7, below 22 and more rows per expert, one tile and several
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("counts", INT4_COUNTS)
+@pytest.mark.parametrize("group,K", [(32, 160), (32, 96), (64, 192), (64, 64), (128, 384)])
+@pytest.mark.parametrize("gather", [True, False])
+def test_a_large_last_scale_at_a_depth_that_ends_inside_a_tile(wq, kind, counts, group, K, gather):
+    """Scale 6000, zero point 15, codes 8 .. 15 in the last group: every weight is finite (at most 42000 in size), though
+    6000 * (0 - 15) would not be in fp16.  The tolerance is that of the other INT4 products."""
+    N, T = 72, sum(counts)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    codes = torch.randint(0, 16, (2, N, K), device="cuda", generator=g)
+    zeros = torch.randint(0, 16, (2, N, K // group), device="cuda", generator=g)
+    scales = (torch.rand(2, N, K // group, device="cuda", generator=g) * 0.01).half()
+    codes[..., -group:] |= 8
+    zeros[..., -1], scales[..., -1] = 15, 6000.0
+    w = ((codes - zeros.repeat_interleave(group, -1)).double() * scales.double().repeat_interleave(group, -1))
+    x = torch.randn(T, K, device="cuda", generator=g)
+    x[:, -group:] *= 2.0 ** -12
+    x = x.to(torch.float16 if kind == "fp16" else torch.bfloat16)
+    off = offsets(counts)
+    rows = torch.randperm(T, device="cuda", generator=g).to(torch.int32) if gather else None
+    y = wq.grouped_gemm_w4a16(x, pack(codes), scales, pack(zeros), off, rows, group)
+    ref, tol, _ = product_ref(kind, x.double(), w, rows, off.cpu(), T, K, False)
+    assert ((y.double() - ref).abs() <= tol).all()
