@@ -126,12 +126,12 @@ template <bool BF>
 struct GroupConst {
     uint32_t zc, hi, lo;
     // fp16: -(1024 + z), -(64 + z) and s.  bf16: -(128 + z) twice, and s = hi + lo, two bf16 values that
-    // hold the 11 bits of s.
+    // hold the 11 bits of s (an infinite s: lo is zero).
     __device__ __forceinline__ void set(uint32_t s16, uint32_t z) {
         if (BF) {
             const float s = half_bits_to_float((uint16_t)s16);
             const uint32_t h = float_to_bf16_bits_rn(s);
-            const uint32_t l = float_to_bf16_bits_rn(s - __uint_as_float(h << 16));
+            const uint32_t l = isinf(s) ? 0u : float_to_bf16_bits_rn(s - __uint_as_float(h << 16));
             zc = 0xC300C300u + z * 0x00010001u;
             hi = h * 0x00010001u;
             lo = l * 0x00010001u;

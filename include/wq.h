@@ -477,6 +477,9 @@ wq_status wq_moe_route(const void *logits, wq_dtype dtype, int T, int E, int top
  * against the experts, or R, whichever are fewer) each s (q - z) is rounded to
  * the type of x, as in wq_gemm_w4a16; below, it is not: the codes are
  * multiplied exactly and each group's sum is scaled in fp32.
+ * An infinite scale then gives an infinity of the group sum's sign (NaN for a
+ * sum of 0), and with at least 22 rows NaN as soon as the group's products
+ * differ in sign or one of them is 0.
  * E <= 512, E * N < 2^31, T, R and K <= 2^29.  w4a16: group_size in {32, 64, 128, 256}, K a
  * multiple of it.  w8a8 and fp8: K % 16 == 0 (w8a8: K <= 131056).  swiglu:
  * N even.

@@ -137,3 +137,25 @@ def test_a_large_last_scale_at_a_depth_that_ends_inside_a_tile(wq, kind, counts,
     y = wq.grouped_gemm_w4a16(x, pack(codes), scales, pack(zeros), off, rows, group)
     ref, tol, _ = product_ref(kind, x.double(), w, rows, off.cpu(), T, K, False)
     assert ((y.double() - ref).abs() <= tol).all()
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("counts", INT4_COUNTS)
+@pytest.mark.parametrize("group,K", [(32, 160), (64, 192), (128, 384), (128, 256), (256, 256)])
+def test_an_infinite_last_scale_gives_infinities(wq, kind, counts, group, K):
+    """All products of the last group have one sign, so that the sum is that infinity whichever kernel takes the rows."""
+    N, T = 40, sum(counts)
+    (q, s, z), _ = make_weights(kind, 2, N, K, group, 4)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    codes = torch.randint(0, 16, (2, N, K), device="cuda", generator=g)
+    codes[..., -group:] = torch.randint(0, 7, (2, N, group), device="cuda", generator=g)
+    zeros = torch.randint(0, 16, (2, N, K // group), device="cuda", generator=g)
+    zeros[..., -1] = 7
+    s = s.clone()
+    s[:, ::2, -1] = math.inf
+    (x,), _ = make_x(kind, T, K, 4)
+    x = x.abs() + 0.125
+    y = wq.grouped_gemm_w4a16(x, pack(codes), s, pack(zeros), offsets(counts), group_size=group)
+    assert (y[:, ::2] == -math.inf).all()
+    assert torch.isfinite(y[:, 1::2]).all()
