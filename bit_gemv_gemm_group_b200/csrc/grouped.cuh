@@ -168,9 +168,15 @@ __device__ __forceinline__ uint4 permute_x(uint4 v) {
                       prmt(v.y, v.w, 0x7632u));
 }
 
-// silu(g) u.  The fast exponential and division are off by a few fp32 units, far below the 16-bit
-// rounding that follows.
-__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+// silu(g) u.  With e = exp(-|g|) <= 1, silu(g) = g / (1 + e) or g e / (1 + e): nothing overflows, and a gate far below
+// zero keeps its value until e itself is below fp32's subnormals (g = -103).  The fast exponential is off by at most
+// 2 + 1.2 |g| units and the fast division (divisors of 1 to 2) by 2: less than 2^-16 for every g whose silu is not
+// subnormal, far below the 16-bit rounding that follows.  An IEEE division costs 18.4 against 15.7 us in 903 rows of 20
+// FP8 experts of 1000 x 1360.
+__device__ __forceinline__ float swiglu(float g, float u) {
+    const float e = __expf(-fabsf(g));
+    return __fdividef(g < 0.0f ? g * e : g, 1.0f + e) * u;
+}
 
 // Two values rounded to fp16 or bf16, the first in the low half: one instruction, where a conversion of a single
 // value takes the quarter-rate pipe.

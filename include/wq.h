@@ -23,7 +23,8 @@
  *    activations are [B or M][K], outputs are [B or M][N].
  *  - fp16 data is passed as uint16_t bit patterns (IEEE 754 binary16).
  *  - Rounding is round-half-to-even everywhere; every division is an IEEE
- *    fp32 division; the library is built without fast-math.
+ *    fp32 division, silu's excepted (see the expert products); the library is
+ *    built without fast-math.
  *  - On a precondition violation the call returns an error status, launches
  *    nothing and records a message readable with wq_last_error() (per host
  *    thread).  Launch failures return WQ_ERR_CUDA.
@@ -459,7 +460,9 @@ wq_status wq_moe_route(const void *logits, wq_dtype dtype, int T, int E, int top
  *   d[n] = sum_k W_e[n][k] * x[rows ? rows[p] : p][k]
  *   y[p][n] = round(d[n])                             (swiglu == 0, y [R][N])
  *   y[p][i] = round(silu(d[i]) * d[N/2 + i])          (swiglu != 0, y [R][N/2])
- * with silu(g) = g / (1 + exp(-g)) in fp32 and one rounding.  d per format:
+ * with silu(g) = g / (1 + exp(-g)) in fp32, by a fast exponential and division
+ * that are off by at most (6 + 1.2 |g|) 2^-23 of it together, and one rounding.
+ * d per format:
  *   w4a16, w4a16_bf16:  W_e[n][k] = s (q - z), x and y fp16 or bf16, fp32
  *       accumulation (order unspecified); rounding of the weights: see below
  *   w8a8:  (float)(int32 sum of codes) * sx[token] * sw[e][n]

@@ -159,3 +159,66 @@ def test_an_infinite_last_scale_gives_infinities(wq, kind, counts, group, K):
     y = wq.grouped_gemm_w4a16(x, pack(codes), s, pack(zeros), offsets(counts), group_size=group)
     assert (y[:, ::2] == -math.inf).all()
     assert torch.isfinite(y[:, 1::2]).all()
+
+
+# ------------------------------------------------------------------------------------------------ SwiGLU far from zero
+FAR_GATES = [-89.5, -88.5, -88.0, -87.5, -87.0, -80.0, -30.0, -1.0, 0.5, 30.0, 88.5, 1000.0]
+
+
+def check_far(y, gates, up, u):
+    """y against silu(gates) up in fp64: u for the type of y; 2 + 1.2 |g| units (2^-23) for the exponential, which turns
+    subnormal below g = -87.3 (a unit of 2^-149 of it), two for the division and half of one each for the other three
+    operations."""
+    g = torch.tensor(gates, dtype=torch.float64, device="cuda")
+    ref = g * torch.sigmoid(g) * up
+    e = torch.exp(-g.abs())
+    rel = u + (6 + 1.2 * g.abs()) * 2.0 ** -23 + torch.where(g < 0, 2.0 ** -149 / e, 0.0)
+    err = (y.double() - ref).abs()
+    assert (err <= ref.abs() * rel * 1.001 + 2.0 ** -25 * (y.dtype is torch.float16)).all(), (err / ref.abs()).tolist()
+
+
+@gpu
+@pytest.mark.parametrize("rows_per_expert", [1, 12, 64])
+def test_swiglu_of_far_gates_int4(wq, rows_per_expert):
+    """bf16, 128 depths of which the first is the gate's and the second the up's: silu(g) 2^100 is an ordinary value where
+    exp(-g) is close to the end of fp32 and beyond."""
+    K, I = 128, 24
+    codes = torch.zeros(1, 2 * I, K, dtype=torch.int64, device="cuda")
+    codes[0, :I, 0] = codes[0, I:, 1] = 1
+    scales = torch.ones(1, 2 * I, 1, dtype=torch.float16, device="cuda")
+    zeros = torch.zeros(1, 2 * I, 1, dtype=torch.int64, device="cuda")
+    T = rows_per_expert
+    gates = [FAR_GATES[i % len(FAR_GATES)] for i in range(max(T, len(FAR_GATES)))]
+    for start in range(0, len(gates), T):
+        part = gates[start:start + T] + [0.5] * (start + T - min(start + T, len(gates)))
+        x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+        x[:, 0], x[:, 1] = torch.tensor(part, device="cuda").bfloat16(), 2.0 ** 100
+        assert x[:, 0].tolist() == part
+        y = wq.grouped_gemm_w4a16(x, pack(codes), scales, pack(zeros), offsets([T]), None, K, swiglu=True)
+        for col in (0, I - 1):
+            check_far(y[:, col], part, 2.0 ** 100, 2.0 ** -8)
+
+
+@gpu
+@pytest.mark.parametrize("T", [12, 200])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_swiglu_of_far_gates_8_bits(wq, T, fp8):
+    K, I = 64, 40
+    one = 0x38 if fp8 else 1                                # E4M3's 1.0
+    gates = (FAR_GATES * 20)[:T]
+    dt = torch.uint8 if fp8 else torch.int8
+    q = torch.zeros(1, 2 * I, K, dtype=dt, device="cuda")
+    q[0, :I, 0] = q[0, I:, 1] = one
+    sw = torch.ones(1, 2 * I, device="cuda")
+    sw[0, I:] = 2.0 ** 104                                  # codes are +-1: the gate is +-sx, the up value sx 2^104
+    g = torch.tensor(gates, device="cuda")
+    xq = torch.zeros(T, K, dtype=dt, device="cuda")
+    xq[:, 0] = torch.where(g < 0, 0xB8 if fp8 else -1, one).to(dt)
+    xq[:, 1] = one
+    sx = g.abs()
+    fn = wq.grouped_gemm_fp8 if fp8 else wq.grouped_gemm_w8a8
+    y = fn(xq, sx, q, sw, offsets([T]), swiglu=True)
+    far = [i for i, v in enumerate(gates) if v < -86]
+    for col in (0, I - 1):
+        for i in far:
+            check_far(y[i:i + 1, col], [gates[i]], 2.0 ** 104 * abs(gates[i]), 2.0 ** -11)
