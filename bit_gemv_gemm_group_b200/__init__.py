@@ -726,10 +726,20 @@ def moe_combine(y, weights, slots, out=None, stream=None):
     return out
 
 
+def _layer_inputs(x, logits, dtypes) -> None:
+    _cuda(x, "x", dtypes, 2)
+    _cuda(logits, "logits", (torch.float32, torch.float16, torch.bfloat16), 2)
+    if logits.shape[0] != x.shape[0]:
+        raise ValueError(f"logits are of {logits.shape[0]} tokens, x of {x.shape[0]}")
+    if logits.device != x.device:
+        raise ValueError(f"logits is on {logits.device}, expected {x.device}")
+
+
 def moe_mlp_w4a16(x, logits, gate_up, down, top_k: int, group_size: int = 128, renormalize: bool = True, stream=None):
     """A mixture-of-experts feed-forward layer with INT4 experts: router, gate and up projection with SwiGLU, down
     projection, combine.  x [T, K] fp16 or bf16, logits [T, E]; gate_up and down are (qweight, scales, qzeros) stacked
     over the experts, [E, 2 I, ...] over K and [E, N, ...] over I.  -> [T, N] in x's dtype."""
+    _layer_inputs(x, logits, (torch.float16, torch.bfloat16))
     with _enter(x, stream):
         _, weights, offsets, rows, slots = moe_route(logits, top_k, renormalize)
         h = grouped_gemm_w4a16(x, *gate_up, offsets, rows, group_size, swiglu=True)
@@ -740,6 +750,7 @@ def moe_mlp_w4a16(x, logits, gate_up, down, top_k: int, group_size: int = 128, r
 def moe_mlp_w8a8(x, logits, gate_up, down, top_k: int, renormalize: bool = True, stream=None):
     """The same layer with INT8 experts: x fp16 [T, K] and the SwiGLU outputs are quantized per token; gate_up and
     down are (wq, sw) stacked over the experts.  -> fp16 [T, N]."""
+    _layer_inputs(x, logits, (torch.float16,))
     with _enter(x, stream):
         _, weights, offsets, rows, slots = moe_route(logits, top_k, renormalize)
         xq, sx = quantize_int8_per_token(x)

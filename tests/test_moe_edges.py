@@ -102,6 +102,32 @@ def test_sizes_past_32_bits_are_refused(wq):
                              torch.zeros(2, dtype=torch.int32, device="cuda"), rows)
 
 
+@gpu
+@pytest.mark.parametrize("kind", ["w8a8", "fp16", "bf16"])
+def test_a_layer_whose_logits_are_of_other_tokens_is_refused(wq, kind):
+    """More logits than rows of x would give zeros for the rest, fewer would leave rows of x out."""
+    E, K, I, N, T = 4, 64, 32, 48, 6
+    up, _ = make_weights(kind, E, 2 * I, K, 32, 1)
+    down, _ = make_weights(kind, E, N, I, 32, 2)
+    dt = torch.bfloat16 if kind == "bf16" else torch.float16
+
+    def layer(x, logits):
+        return wq.moe_mlp_w8a8(x, logits, up, down, 2) if kind == "w8a8" else wq.moe_mlp_w4a16(x, logits, up, down, 2, 32)
+
+    x = torch.randn(T, K, device="cuda").to(dt)
+    assert layer(x, torch.randn(T, E, device="cuda")).shape == (T, N)
+    for tokens in (T - 1, T + 1):
+        with pytest.raises(ValueError, match="tokens"):
+            layer(x, torch.randn(tokens, E, device="cuda"))
+    for bad in (torch.randn(T, E), torch.randn(T, E, device="cuda").double(), torch.randn(T, 2 * E, device="cuda")[:, ::2],
+                torch.randn(T, E + 1, device="cuda"), None):
+        with pytest.raises((ValueError, TypeError)):
+            layer(x, bad)
+    for bad in (x.cpu(), x.float(), x.t(), x[0], None):
+        with pytest.raises((ValueError, TypeError)):
+            layer(bad, torch.randn(T, E, device="cuda"))
+
+
 # ------------------------------------------------------------------------------------------------ depth and scales
 def pack(codes):
     """[..., n] 4-bit codes -> int32 words of eight, lowest bits first."""
