@@ -453,7 +453,16 @@ extern "C" wq_status wq_moe_route(const void *logits, wq_dtype dtype, int T, int
                "wq_moe_route: E (%d) must be at most %d and top_k (%d) at most %d", E, MAX_E, top_k, MAX_K);
     WQ_REQUIRE(T <= MAX_T && (long long)T * top_k <= INT_MAX, WQ_ERR_UNSUPPORTED,
                "wq_moe_route: T (%d) must be at most %d, and T * top_k below 2^31", T, MAX_T);
-    if (wq_moe_route_workspace_bytes(T, E)) WQ_REQUIRE_PTR(workspace, "workspace");
+    const size_t ws_bytes = wq_moe_route_workspace_bytes(T, E), pairs = (size_t)T * top_k * 4;
+    if (ws_bytes) WQ_REQUIRE_PTR(workspace, "workspace");
+    // Blocks write while others still read, so no two of these may share memory.
+    const struct { const void *p; size_t n; } part[] = {
+        {logits, (size_t)T * E * (dtype == WQ_F32 ? 4 : 2)}, {ids, pairs}, {weights, pairs}, {rows, pairs}, {slots, pairs},
+        {offsets, ((size_t)E + 1) * 4}, {workspace, ws_bytes}};
+    for (int i = 0; i < 7; ++i)
+        for (int j = 0; j < i; ++j)
+            WQ_REQUIRE(!(part[i].n && overlap(part[i].p, part[i].n, part[j].p, part[j].n)), WQ_ERR_INVALID_ARG,
+                       "wq_moe_route: an output or the workspace overlaps another argument");
     const RouteArgs a{T, E, top_k, tokens_per_block(T), ids, weights, offsets, rows, slots,
                       static_cast<uint16_t *>(workspace)};
     cudaStream_t st = as_stream(stream);

@@ -448,6 +448,7 @@ wq_status wq_awq(const uint16_t *w, int N, int K, int group_size, const uint16_t
  * rows: out int32 [T * top_k];  slots: out int32 [T][top_k].  workspace:
  * wq_moe_route_workspace_bytes(T, E) bytes (0, and NULL is taken, for T <= 64),
  * 16-byte aligned, contents on entry do not matter; calls that share one must not overlap on the GPU.
+ * Outputs or a workspace that overlap each other or the logits are refused.
  * 1 <= top_k <= min(E, 32), E <= 512, T <= 2^23, T * top_k < 2^31.
  */
 size_t wq_moe_route_workspace_bytes(int T, int E);

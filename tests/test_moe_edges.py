@@ -1,6 +1,7 @@
 """Mixture-of-experts operators at their edges: calls that give up, depths and scales that end inside a tile, far values,
 arguments that do not fit together.  The references and tolerances are those of test_moe.py unless a test derives its own.
 """
+import ctypes
 import math
 
 import numpy as np
@@ -126,6 +127,27 @@ def test_a_layer_whose_logits_are_of_other_tokens_is_refused(wq, kind):
     for bad in (x.cpu(), x.float(), x.t(), x[0], None):
         with pytest.raises((ValueError, TypeError)):
             layer(bad, torch.randn(T, E, device="cuda"))
+
+
+@pytest.mark.parametrize("T", [40, 300])
+@pytest.mark.parametrize("dtype", [0, 2])
+def test_router_arguments_that_overlap_are_refused(wq, T, dtype):
+    """Each pair of the logits, the five outputs and the workspace, at the first, the last and the bytes before."""
+    E, k = 24, 3
+    ws = wq.moe_route_workspace_bytes(T, E)
+    size = [T * E * (2 if dtype else 4), T * k * 4, T * k * 4, (E + 1) * 4, T * k * 4, T * k * 4, ws]
+    for i in range(7):
+        for j in range(7):
+            if i == j or not (size[i] and size[j]):
+                continue
+            base = 0x1000000
+            for at in (0, (size[i] - 1) // 16 * 16, 16 - (size[j] + 15) // 16 * 16):
+                if at < 0 and at + size[j] <= 0:
+                    continue
+                p = [ctypes.c_void_p((n + 2) << 32) for n in range(7)]
+                p[i], p[j] = ctypes.c_void_p(base), ctypes.c_void_p(base + at)
+                status = wq.lib.wq_moe_route(p[0], dtype, T, E, k, 1, *p[1:], None)
+                assert status == wq.WQ_ERR_INVALID_ARG and b"overlaps" in wq.lib.wq_last_error(), (i, j, at)
 
 
 # ------------------------------------------------------------------------------------------------ depth and scales
