@@ -308,6 +308,9 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
                 __syncwarp();
             }
         }
+        // The first CTA's commits arrive on this one's barriers too: all of them have when the drain has.
+        if (warp == 1 && leader) drain_parity(smem_u32(&bar->drain), 0, DRAIN_NS, a.status, SITE_DRAIN);
+        __syncwarp();
     } else if (warp == 1) {
         // -------------------------------------------------------------------- MMA issuer
         const bool leader = elect_one();
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(Layout<KIND, GATHER, PAIR>::THREADS, 1)
             __syncwarp();
         }
         if (leader) {
-            if (PAIR) tc_commit_pair(smem_u32(&bar->drain));
+            if (PAIR) tc_commit_pair_both(smem_u32(&bar->drain));
             else tc_commit(smem_u32(&bar->drain));
             drain_parity(smem_u32(&bar->drain), 0, DRAIN_NS, a.status, SITE_DRAIN);
         }

@@ -41,6 +41,30 @@ def test_few_rows_under_a_tiny_limit_leave_the_device_as_it_was(wq, kind):
     assert wq.device_status() == 0
 
 
+@gpu
+@pytest.mark.parametrize("kind", ["w8a8", "fp8", "fp16", "bf16"])
+def test_pairs_under_a_tiny_limit_leave_the_device_as_it_was(wq, kind):
+    """Neither CTA of a pair leaves while something of the other's is on its way to it: after calls that may have given
+    up, kernels that use the same shared memory otherwise get their results, and so do the pairs."""
+    N, K, counts = 1024, 4096, [200, 90]
+    wa, _ = make_weights(kind, 2, N, K, 128, 2)
+    xa, _ = make_x(kind, sum(counts), K, 2)
+    one, _ = make_x(kind, 3, K, 3)
+    off, few = offsets(counts), offsets([1, 2])
+    good, other = call(wq, kind, xa, wa, off, None, 128, False), call(wq, kind, one, wa, few, None, 128, False)
+    assert wq.device_status() == 0
+    for _ in range(5):
+        try:
+            wq.set_wait_limit(1)
+            call(wq, kind, xa, wa, off, None, 128, False)
+        finally:
+            wq.set_wait_limit(0)
+        assert torch.equal(call(wq, kind, one, wa, few, None, 128, False), other)
+        assert wq.device_status() in (wq.WQ_OK, wq.WQ_ERR_TIMEOUT)
+        assert torch.equal(call(wq, kind, xa, wa, off, None, 128, False), good)
+        assert wq.device_status() == 0
+
+
 # ------------------------------------------------------------------------------------------------ CTAs that share a tile
 @gpu
 @pytest.mark.parametrize("kind,counts,N,K,group", [
