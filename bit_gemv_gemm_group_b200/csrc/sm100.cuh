@@ -124,7 +124,9 @@ __device__ __forceinline__ void fence_acquire_smem() {
 }
 
 // wait_parity for kernels whose other warps need the issue slots: the abort flag and the clock, about 20
-// instructions, are looked at after every 16th test only.  RELAXED: the test is mbar_try_wait_relaxed.
+// instructions, are looked at after every 16th test only.  A test sleeps for up to 8.5 us, so a wait lasts 0.15 ms
+// however short the limit; tests that poll under a short limit cost the few-rows kernel of the expert products 7 to 10%.
+// RELAXED: the test is mbar_try_wait_relaxed.
 template <bool RELAXED = false>
 __device__ __forceinline__ bool wait_parity_lean(uint32_t bar, uint32_t parity, const WaitCtl &c, unsigned site) {
     auto test = [&] { return RELAXED ? mbar_try_wait_relaxed(bar, parity) : mbar_try_wait(bar, parity); };

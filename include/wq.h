@@ -526,7 +526,8 @@ wq_status wq_device_status(void *stream);
  * Wall-clock limit, in nanoseconds, of each bounded wait inside the
  * tensor-core kernels (default 2e9, two seconds; 0 restores the default).
  * Applies to launches made after the call.  Small values exist so that tests
- * can make a wait run out on purpose; the kernel then stops, drains its own
+ * can make a wait run out on purpose (in the expert products a wait lasts
+ * 0.15 ms at least); the kernel then stops, drains its own
  * in-flight copies and tensor-core operations, releases its tensor memory and
  * records WQ_ERR_TIMEOUT for wq_device_status().
  */

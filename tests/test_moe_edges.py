@@ -65,6 +65,39 @@ def test_pairs_under_a_tiny_limit_leave_the_device_as_it_was(wq, kind):
         assert wq.device_status() == 0
 
 
+@gpu
+@pytest.mark.parametrize("kind,counts", [
+    ("w8a8", [200, 90]), ("fp8", [200, 90]), ("fp16", [200, 90]), ("bf16", [200, 90]),      # pairs
+    ("w8a8", [9, 14]), ("fp8", [9, 14])])                                                   # single CTAs
+def test_waits_that_ran_out_are_reported(wq, kind, counts):
+    """Tiles of a third of a millisecond, for which the epilogue waits longer than a wait lasts under a tiny limit (about
+    0.15 ms): the calls end and say so, and the next ones are right.  (Neither of the other INT4 kernels has such a wait.)"""
+    N, K, T = 9472, 131056 if kind == "w8a8" else 131072, sum(counts)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    if kind in ("fp16", "bf16"):
+        w = torch.randint(-2 ** 31, 2 ** 31, (2, N, K // 8), dtype=torch.int32, device="cuda", generator=g)
+        wa = (w, torch.full((2, N, K // 128), 2.0 ** -9, dtype=torch.float16, device="cuda"),
+              torch.full((2, N, K // 1024), 0x77777777, dtype=torch.int32, device="cuda"))
+    else:
+        w = torch.randint(0, 127, (2, N, K), dtype=torch.int8, device="cuda", generator=g)
+        wa = (w if kind == "w8a8" else w.view(torch.uint8), torch.full((2, N), 2.0 ** -20, device="cuda"))
+    xa, _ = make_x(kind, T, K, 2)
+    off, rows = offsets(counts), torch.randperm(T, device="cuda").to(torch.int32)
+    for r, swiglu in ((rows, False), (None, True)):
+        good = call(wq, kind, xa, wa, off, r, 128, swiglu)
+        assert wq.device_status() == 0
+        for _ in range(3):
+            try:
+                wq.set_wait_limit(1)
+                call(wq, kind, xa, wa, off, r, 128, swiglu)
+                assert wq.device_status() == wq.WQ_ERR_TIMEOUT
+            finally:
+                wq.set_wait_limit(0)
+            again = call(wq, kind, xa, wa, off, r, 128, swiglu)
+            assert torch.equal(again.view(torch.int16), good.view(torch.int16))
+            assert wq.device_status() == 0
+
+
 # ------------------------------------------------------------------------------------------------ CTAs that share a tile
 @gpu
 @pytest.mark.parametrize("kind,counts,N,K,group", [
