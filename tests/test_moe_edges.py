@@ -327,3 +327,66 @@ def test_swiglu_of_far_gates_8_bits(wq, T, fp8):
     for col in (0, I - 1):
         for i in far:
             check_far(y[i:i + 1, col], [gates[i]], 2.0 ** 104 * abs(gates[i]), 2.0 ** -11)
+
+
+# ------------------------------------------------------------------------------------------------ offsets, NaN in large batches
+SENTINEL = 77.0
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["w8a8", "fp8", "fp16", "bf16"])
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("swiglu", [True, False])
+def test_bad_offsets_of_large_batches_stay_in_bounds(wq, kind, gather, swiglu):
+    """Pairs of CTAs: offsets out of range or decreasing are clamped to [0, R] and made non-decreasing, with rows that
+    repeat and lie outside x; guard rows around y stay as they are."""
+    R, E, N, K = 700, 4, 136, 160
+    wa, w = make_weights(kind, E, N, K, 32, 3)
+    xa, x = make_x(kind, R, K, 3)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    rows = torch.randint(-2, R + 2, (R,), device="cuda", generator=g).to(torch.int32) if gather else None
+    dt = torch.bfloat16 if kind == "bf16" else torch.float16
+    for raw in ([-7, 400, 5, 2000, 300], [800, 900, 701, 0, 90], [0, -1, -2, -3, 2 ** 31 - 1],
+                [-2 ** 31, 2 ** 31 - 1, 0, 0, 0], [3, 260, 260, 517, 690]):
+        fixed = np.maximum.accumulate(np.clip(raw, 0, R))
+        off = torch.tensor(raw, dtype=torch.int32, device="cuda")
+        cols = N // 2 if swiglu else N
+        guarded = torch.full((R + 32, cols), SENTINEL, dtype=dt, device="cuda")
+        out = guarded[16:-16]
+        call(wq, kind, xa, wa, off, rows, 32, swiglu, out)
+        y, tol, written = product_ref(kind, x, w, rows, fixed, R, K, swiglu)
+        assert ((out.double() - y).abs() <= tol)[written].all()
+        assert (out[~written] == SENTINEL).all()
+        assert (guarded[:16] == SENTINEL).all() and (guarded[-16:] == SENTINEL).all()
+    assert wq.device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16", "fp8"])
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("swiglu", [True, False])
+def test_nan_and_inf_stay_in_their_row_of_a_large_batch(wq, kind, gather, swiglu):
+    """Pairs of CTAs, both halves of a tile, rows next to padding: a dirty row changes its own outputs only."""
+    counts, N, K = [90, 300, 41], 136, 288
+    T = sum(counts)
+    wa, _ = make_weights(kind, 3, N, K, 32, 9)
+    xa, _ = make_x(kind, T, K, 9)
+    dirty = xa[0].clone()
+    where = [0, 3, 89, 90, 245, 389, 390, T - 1]
+    for n, p in enumerate(where):
+        if kind == "fp8":
+            dirty[p, (37 * n) % K] = 0x7F if n % 2 else 0xFF
+        else:
+            dirty[p, (37 * n) % K] = math.nan if n % 2 else math.inf
+    off = offsets(counts)
+    rows = torch.arange(T, device="cuda", dtype=torch.int32).flip(0) if gather else None
+    clean_y = call(wq, kind, xa, wa, off, rows, 32, swiglu)
+    y = call(wq, kind, (dirty, *xa[1:]), wa, off, rows, 32, swiglu)
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[[T - 1 - p for p in where] if gather else where] = False
+    assert torch.equal(y[keep], clean_y[keep])
+    bad = y[~keep].float()
+    if kind == "fp8":
+        assert torch.isnan(bad).all()
+    elif not swiglu:
+        assert not torch.isfinite(bad).any()
