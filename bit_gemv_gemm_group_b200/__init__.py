@@ -755,6 +755,8 @@ def moe_mlp_w8a8(x, logits, gate_up, down, top_k: int, renormalize: bool = True,
         _, weights, offsets, rows, slots = moe_route(logits, top_k, renormalize)
         xq, sx = quantize_int8_per_token(x)
         h = grouped_gemm_w8a8(xq, sx, *gate_up, offsets, rows, swiglu=True)
+        # Rows of pairs without an expert are as the allocation left them, in h and in all that is made of it: every row
+        # is quantized by itself, whatever its bits, and neither the product nor the combine reads those.
         hq, sh = quantize_int8_per_token(h)
         y = grouped_gemm_w8a8(hq, sh, *down, offsets)
         return moe_combine(y, weights, slots)

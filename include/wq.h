@@ -109,6 +109,8 @@ wq_status wq_quantize_int8_per_channel(const uint16_t *w, int N, int K, const fl
  *   q[m][k] = clamp(rne(x'_k / scales[m]), -128, 127)
  * x: fp16 [M][K];  smooth: nullable fp32 [K];  q: out int8 [M][K];
  * scales: out fp32 [M].  K % 16 == 0.
+ * A row with NaN or infinities gets codes and a scale without meaning; no
+ * other row is affected.
  */
 wq_status wq_quantize_int8_per_token(const uint16_t *x, int M, int K, const float *smooth,
                                      int8_t *q, float *scales, void *stream);

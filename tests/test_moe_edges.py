@@ -390,3 +390,48 @@ def test_nan_and_inf_stay_in_their_row_of_a_large_batch(wq, kind, gather, swiglu
         assert torch.isnan(bad).all()
     elif not swiglu:
         assert not torch.isfinite(bad).any()
+
+
+# ------------------------------------------------------------------------------------------------ rows that nothing wrote
+@gpu
+@pytest.mark.parametrize("K", [16, 320, 4112, 8208, 16400])
+def test_the_token_quantizer_takes_any_bits_row_by_row(wq, K):
+    """Rows of any bits, NaN and infinities among them, change nothing in the other rows, whichever kernel takes the
+    depth (the last two: two CTAs a row, and two passes)."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn(70, K, device="cuda", generator=g).half()
+    q, s = wq.quantize_int8_per_token(x)
+    dirty = torch.arange(70, device="cuda") % 3 == 1
+    x.view(torch.int16)[dirty] = torch.randint(-2 ** 15, 2 ** 15, (int(dirty.sum()), K), device="cuda", generator=g).short()
+    x[1], x[4] = math.nan, math.inf
+    q2, s2 = wq.quantize_int8_per_token(x)
+    assert torch.equal(q2[~dirty], q[~dirty]) and torch.equal(s2[~dirty], s[~dirty])
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["w8a8", "fp16", "bf16"])
+@pytest.mark.parametrize("T", [9, 300])
+@pytest.mark.parametrize("bits", [0x7FFF, 0x7C00, 0xFFFF])
+def test_a_layer_does_not_see_what_its_memory_held(wq, kind, T, bits):
+    """Padded tokens leave rows of the products unwritten: with every byte of the allocator's cache NaN or infinity, the
+    layer's result is the same, finite, and zero for those tokens."""
+    E, k, K, I, N = 6, 2, 128, 512, 160
+    g = torch.Generator(device="cuda").manual_seed(T)
+    up, _ = make_weights(kind, E, 2 * I, K, 64, 1)
+    down, _ = make_weights(kind, E, N, I, 64, 2)
+    x = torch.randn(T, K, device="cuda", generator=g).to(torch.bfloat16 if kind == "bf16" else torch.float16)
+    logits = torch.randn(T, E, device="cuda", generator=g)
+    logits[1::2] = -math.inf
+
+    def layer(fill):
+        sizes = [T * k * I * 2, T * k * N * 2, T * N * 2, T * k * I, T * K, T * k * 4, T * 4, 1 << 12, 1 << 16]
+        held = [torch.full((n // 2 + 256,), fill, dtype=torch.int16, device="cuda") for n in sizes for _ in range(4)]
+        torch.cuda.synchronize()
+        del held
+        if kind == "w8a8":
+            return wq.moe_mlp_w8a8(x, logits, up, down, k)
+        return wq.moe_mlp_w4a16(x, logits, up, down, k, 64)
+
+    clean = layer(0)
+    assert torch.isfinite(clean).all() and (clean[1::2] == 0).all() and float(clean[::2].abs().max()) > 0
+    assert torch.equal(layer(bits - (1 << 16) if bits >= 1 << 15 else bits), clean)
