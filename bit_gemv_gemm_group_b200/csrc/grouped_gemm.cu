@@ -102,10 +102,9 @@ __device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, uin
         if (KIND == K_I8) mma_i8_pair(d, a, b, idesc, acc);
         else if (KIND == K_FP8) mma_f8f6f4_pair(d, a, b, idesc, acc);
         else mma_f16_pair(d, a, b, idesc, acc);
-    } else {
+    } else {   // INT4 comes in pairs only
         if (KIND == K_I8) mma_i8(d, a, b, idesc, acc);
-        else if (KIND == K_FP8) mma_f8f6f4(d, a, b, idesc, acc);
-        else mma_f16(d, a, b, idesc, acc);
+        else mma_f8f6f4(d, a, b, idesc, acc);
     }
 }
 

@@ -315,17 +315,6 @@ __host__ __device__ constexpr uint32_t idesc_sf_bytes(uint32_t idesc, uint32_t a
     return idesc | (b_byte << 4) | (a_byte << 29);
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, kind::f16 (fp16/bf16 -> fp32).
-__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 // kind::f16 MMA with A (M x 16, 128 lanes by 8 columns of fp16 pairs) read from tensor
 // memory at a_tmem and B from shared memory.
 __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
