@@ -612,7 +612,7 @@ def _grouped(x, offsets, rows, E, N, swiglu, out, dtype):
     T = R = x.shape[0]
     _with(x, offsets, "offsets", torch.int32, (E + 1,))
     if rows is not None:
-        R = rows.numel()
+        R = _cuda(rows, "rows", (torch.int32,), 1).shape[0]
         _with(x, rows, "rows", torch.int32, (R,))
     _int32(T=T, R=R, N=N, K=x.shape[1])
     if swiglu and N % 2:
@@ -688,6 +688,8 @@ def grouped_gemm_fp8(xq, sx, wq, sw, offsets, rows=None, swiglu: bool = False, o
     _cuda(wq, "wq", (torch.uint8,), 3)
     E, N, K = wq.shape
     _with(xq, wq, "wq", torch.uint8, (E, N, xq.shape[1]))
+    _cuda(sx, "sx", (torch.float32,))
+    _cuda(sw, "sw", (torch.float32,))
     if sx.shape not in ((xq.shape[0],), (1,)) or sw.shape not in ((E, N), (E,)):
         raise ValueError("shape mismatch: sx must be [T] or [1], sw [E, N] or [E]")
     _with(xq, sx, "sx", torch.float32, sx.shape)

@@ -186,6 +186,26 @@ def test_a_layer_whose_logits_are_of_other_tokens_is_refused(wq, kind):
             layer(bad, torch.randn(T, E, device="cuda"))
 
 
+@gpu
+def test_arguments_that_are_no_tensors_are_refused_as_such(wq):
+    """As everywhere in the binding: TypeError, with the argument's name."""
+    T, E, N, K = 4, 2, 16, 32
+    x = torch.zeros(T, K, dtype=torch.uint8, device="cuda")
+    w = torch.zeros(E, N, K, dtype=torch.uint8, device="cuda")
+    sx, sw, off = torch.ones(T, device="cuda"), torch.ones(E, N, device="cuda"), offsets([1, 3])
+    rows = torch.zeros(T, dtype=torch.int32, device="cuda")
+    good = [x, sx, w, sw, off, rows]
+    wq.grouped_gemm_fp8(*good)
+    for n, name in enumerate(("xq", "sx", "wq", "sw", "offsets", "rows")):
+        for bad in ([0, 1], 0.5, np.zeros(4, np.int32)):
+            args = list(good)
+            args[n] = bad
+            with pytest.raises(TypeError, match=name):
+                wq.grouped_gemm_fp8(*args)
+    with pytest.raises(ValueError, match="rows"):
+        wq.grouped_gemm_fp8(*good[:5], rows.view(2, 2))
+
+
 @pytest.mark.parametrize("T", [40, 300])
 @pytest.mark.parametrize("dtype", [0, 2])
 def test_router_arguments_that_overlap_are_refused(wq, T, dtype):
