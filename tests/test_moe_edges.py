@@ -455,3 +455,51 @@ def test_a_layer_does_not_see_what_its_memory_held(wq, kind, T, bits):
     clean = layer(0)
     assert torch.isfinite(clean).all() and (clean[1::2] == 0).all() and float(clean[::2].abs().max()) > 0
     assert torch.equal(layer(bits - (1 << 16) if bits >= 1 << 15 else bits), clean)
+
+
+# ------------------------------------------------------------------------------------------------ rounding of INT4 weights
+def to_bits(w, bits):
+    """fp64 values rounded to `bits` significant bits, ties to even."""
+    m, e = torch.frexp(w)
+    return torch.ldexp(torch.round(m * 2.0 ** bits), e - bits)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("counts,rounded", [([3, 8], False), ([12, 30], False), ([23, 21], True), ([300, 90], True)])
+@pytest.mark.parametrize("group", [32, 128])
+def test_int4_weights_are_rounded_where_the_header_says(wq, kind, counts, rounded, group):
+    """From 22 rows per expert on, y is the product of s (q - z) rounded to x's type; below, of s (q - z) itself.  bf16
+    takes s in two parts there, (q - z) hi + round((q - z) lo), rounded once more.
+    A row of x has eight entries of +-1, so that the fp32 sums are off by at most 8 2^-23 S and what is left is the
+    output's rounding u |y|.  Where the terms cancel (|y| below a tenth of one, about 3% of the outputs) the weights'
+    roundings, u / 2 of a term at most each, are far larger: no output may be outside for the one form, some are for the
+    other."""
+    N, K, T = 128, 2048, sum(counts)
+    g = torch.Generator(device="cuda").manual_seed(group)
+    codes = torch.randint(0, 16, (2, N, K), device="cuda", generator=g)
+    zeros = torch.randint(0, 16, (2, N, K // group), device="cuda", generator=g)
+    scales = torch.exp(torch.randn(2, N, K // group, device="cuda", generator=g) * 0.5 - 5).half()
+    d = (codes - zeros.repeat_interleave(group, -1)).double()
+    s = scales.double().repeat_interleave(group, -1)
+    exact = d * s
+    if kind == "fp16":
+        coarse = to_bits(exact, 11)
+    else:
+        hi = to_bits(s, 8)
+        coarse = to_bits(d * hi + to_bits(d * (s - hi), 8), 8)
+    x = torch.zeros(T, K, dtype=torch.float16 if kind == "fp16" else torch.bfloat16, device="cuda")
+    where = torch.rand(T, K, device="cuda", generator=g).topk(8, dim=1).indices
+    x.scatter_(1, where, torch.randint(0, 2, (T, 8), device="cuda", generator=g).to(x.dtype) * 2 - 1)
+    y = wq.grouped_gemm_w4a16(x, pack(codes), scales, pack(zeros), offsets(counts), group_size=group).double()
+    u, outside = 2.0 ** -11 if kind == "fp16" else 2.0 ** -8, {}
+    for name, w in (("exact", exact), ("rounded", coarse)):
+        at, outside[name] = 0, 0
+        for e, n in enumerate(counts):
+            xe = x[at:at + n].double()
+            ref, size = xe @ w[e].T, xe.abs() @ w[e].abs().T
+            tol = 8 * 2.0 ** -23 * size * (1 + u) + ref.abs() * u + 2.0 ** -25
+            outside[name] += int(((y[at:at + n] - ref).abs() > tol).sum())
+            at += n
+    assert outside["rounded" if rounded else "exact"] == 0, outside
+    assert outside["exact" if rounded else "rounded"] > 0, outside
