@@ -503,3 +503,112 @@ def test_int4_weights_are_rounded_where_the_header_says(wq, kind, counts, rounde
             at += n
     assert outside["rounded" if rounded else "exact"] == 0, outside
     assert outside["exact" if rounded else "rounded"] > 0, outside
+
+
+# ------------------------------------------------------------------------------------------------ streams, graphs, sizes
+@gpu
+@pytest.mark.parametrize("T", [40, 300, 5000])
+def test_routers_on_two_streams_and_in_two_graphs(wq, T):
+    """Calls that overlap share nothing; two graphs of the router, one after the other, may share a workspace, and follow
+    the logits in memory."""
+    E, k = 48, 5
+    g = torch.Generator(device="cuda").manual_seed(T)
+    logits = [torch.randn(T, E, device="cuda", generator=g) for _ in range(2)]
+    good = [wq.moe_route(x, k) for x in logits]
+    y = torch.randn(T * k, 72, device="cuda", generator=g).half()
+    sums = [wq.moe_combine(y, w, slots) for _, w, _, _, slots in good]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        got = []
+        for x, st in zip(logits, streams):
+            r = wq.moe_route(x, k, stream=st)
+            got.append((r, wq.moe_combine(y, r[1], r[4], stream=st)))
+        torch.cuda.synchronize()
+        for (r, out), want, total in zip(got, good, sums):
+            assert all(torch.equal(a, b) for a, b in zip(r, want)) and torch.equal(out, total)
+    workspace = torch.empty(max(16, wq.moe_route_workspace_bytes(T, E)), dtype=torch.uint8, device="cuda")
+    held, graphs, out = torch.empty_like(logits[0]), [], []
+    for renormalize in (True, False):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            out.append(wq.moe_route(held, k, renormalize, workspace=workspace))
+    for x in (*logits, logits[0].neg()):
+        held.copy_(x)
+        workspace.fill_(0xA5)
+        for graph in graphs:
+            graph.replay()
+        for renormalize, got in zip((True, False), out):
+            assert all(torch.equal(a, b) for a, b in zip(got, wq.moe_route(x, k, renormalize)))
+
+
+@gpu
+def test_the_router_at_its_most_tokens(wq):
+    """2^23 tokens, logits past 2^31 elements: a known choice for each token."""
+    T, E = 1 << 23, 300
+    token = torch.arange(T, device="cuda")
+    want = (token * 7919 + (token >> 11)) % E
+    logits = torch.zeros(T, E, dtype=torch.float16, device="cuda")
+    logits.scatter_(1, want[:, None], 4.0)
+    ids, weights, off, rows, slots = wq.moe_route(logits, 1, renormalize=False)
+    assert torch.equal(ids[:, 0].long(), want)
+    p = math.exp(4.0) / (math.exp(4.0) + E - 1)
+    assert float((weights.double() - p).abs().max()) <= 2.0 ** -15 * p
+    assert torch.equal(off.long(), torch.cat([token.new_zeros(1), torch.bincount(want, minlength=E).cumsum(0)]))
+    order = torch.sort(want, stable=True).indices
+    assert torch.equal(rows.long(), order)
+    assert torch.equal(slots[order, 0].long(), token)
+
+
+@gpu
+@pytest.mark.parametrize("N", [16400, 16401])
+def test_a_combine_past_32_bit_offsets(wq, N):
+    """Rows of y and of the result past 2^31 elements."""
+    T, R = 140000, 140001
+    y = torch.empty(R, N, dtype=torch.bfloat16, device="cuda")
+    y.copy_((torch.arange(R, device="cuda") % 251)[:, None] + (torch.arange(N, device="cuda") % 3))
+    slots = torch.arange(T, device="cuda").flip(0).to(torch.int32)[:, None] + 1
+    weights = torch.full((T, 1), 0.5, device="cuda")
+    out = wq.moe_combine(y, weights, slots)
+    for t in (0, 1, 69999, 131071, 131072, T - 1):
+        assert torch.equal(out[t], y[T - t] * 0.5)
+    assert torch.equal(out[:, N - 1], y[1:, N - 1].flip(0) * 0.5)
+
+
+@gpu
+@pytest.mark.parametrize("kind,R", [("fp16", 140000), ("bf16", 140000), ("w8a8", 3000), ("fp16", 3000), ("fp16", 9000)])
+def test_products_past_32_bit_offsets(wq, kind, R):
+    """y past 2^31 elements: pairs of CTAs in order and gathered, single CTAs (6 rows per expert) and both other INT4
+    kernels (6 and 18 rows per expert), whose outputs are as many by their width."""
+    E, K = (3, 32) if R == 140000 else (500, 32)
+    N = 16400 if R == 140000 else (1 << 31) // R + 1000
+    g = torch.Generator(device="cuda").manual_seed(3)
+    counts = [70001, 69989, 10] if R == 140000 else [R // E] * E
+    off = offsets(counts)
+    if kind == "w8a8":
+        wa = (torch.randint(-128, 128, (E, N, K), device="cuda", dtype=torch.int8, generator=g), torch.ones(E, N, device="cuda"))
+        xa = (torch.randint(-128, 128, (R, K), device="cuda", dtype=torch.int8, generator=g), torch.full((R,), 2.0 ** -6, device="cuda"))
+    else:
+        wa = (torch.randint(-2 ** 31, 2 ** 31, (E, N, K // 8), device="cuda", dtype=torch.int32, generator=g),
+              torch.full((E, N, 1), 2.0 ** -6, dtype=torch.float16, device="cuda"),
+              torch.full((E, N, 1), 7, dtype=torch.int32, device="cuda"))
+        xa = (torch.randn(R, K, device="cuda", generator=g).to(torch.bfloat16 if kind == "bf16" else torch.float16),)
+    rows = torch.arange(R, device="cuda", dtype=torch.int32).flip(0)
+    nibbles = torch.arange(0, 32, 4, device="cuda", dtype=torch.int32)
+    u = 2.0 ** -8 if kind == "bf16" else 2.0 ** -11
+    for r in (None, rows):
+        y = call(wq, kind, xa, wa, off, r, 32, False)
+        for p in (0, 1, R // 2, (1 << 31) // N, (1 << 31) // N + 1, R - 2, R - 1):
+            e = int(torch.searchsorted(off.long(), torch.tensor(p, device="cuda"), right=True)) - 1
+            t = R - 1 - p if r is not None else p
+            x = xa[0][t].double()
+            if kind == "w8a8":
+                ref = (wa[0][e].double() @ x) * 2.0 ** -6
+                tol = ref.abs() * (u + 2.0 ** -22) + 2.0 ** -25
+            else:
+                w = (((wa[0][e].unsqueeze(-1) >> nibbles) & 15).view(N, K).double() - 7) * 2.0 ** -6   # exact in 8 bits
+                ref = w @ x
+                tol = K * 2.0 ** -23 * (w.abs() @ x.abs()) * (1 + u) + ref.abs() * u + 2.0 ** -25
+            assert ((y[p].double() - ref).abs() <= tol).all(), p
+        del y
+    assert wq.device_status() == 0
