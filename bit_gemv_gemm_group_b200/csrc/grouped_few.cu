@@ -23,8 +23,9 @@
 //                q - z into tensor memory.  A thread takes 256 codes at a time: with 128 (and twice the warps)
 //                its waits, loads and addresses were 250 of 390 instructions
 //
-// Measured on B200: 8 experts of 28672 x 4096 for 64 rows, fp16, 492 MB, 154 us (3.2 TB/s); 64 experts of
-// 4096 x 2048 for 768 bf16 rows, groups of 64, 297 MB, 146 us (2.0 TB/s).  With the whole dequantization, the fmas,
+// Measured on B200: 8 experts of 28672 x 4096 for 64 rows, fp16, 492 MB, 149 us (3.3 TB/s, floor 76 us); 64 experts of
+// 4096 x 2048 for 768 bf16 rows, groups of 64, 297 MB, 110 us where each has 12 rows and 120 us at random counts, of
+// which those above 16 rows are another tile (2.7 and 2.5 TB/s, floor 46 us).  With the whole dequantization, the fmas,
 // all but one MMA per stage and the loads of x and scales taken out, 440 MB of weights take 94 us against 148: no
 // unit bounds it alone, the loop of a dequantizing group (two thirds of its 1290 cycles per pack are arithmetic
 // at about 5 cycles an instruction) and the rest of the pipeline lie close together.

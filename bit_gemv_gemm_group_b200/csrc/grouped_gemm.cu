@@ -29,11 +29,11 @@
 //               request took 32 cycles for its 512 bytes, four times what the MMAs leave), and for INT4
 //               three groups of four warps that dequantize every third packed tile each
 //
-// Measured on B200, 16384 rows over 32 experts of 4096 x 4096 (0.55 T products, at clocks that the power cap has
-// brought down): INT8 with SwiGLU 234 us (2.35 POPS, 0.69 of twice the bf16 burst rate and 0.81 of twice the
-// sustained one), INT4 with bf16 rows 489 us (1.12 PFLOP/s, 0.77 of the sustained rate; 443 us where the rows
-// already lie in order, 388 us without the dequantization's arithmetic).  16 rows over 8 INT8 experts of
-// 4096 x 14336, 466 MB: 78 us (6.0 TB/s, 0.93 of the copy rate).
+// Measured on B200 (graphs of calls, short ones after a pause for full clocks and long ones for the clocks that the
+// power cap leaves), 16384 rows over 32 experts of 4096 x 4096, 0.55 T products: INT8 with SwiGLU 225 and 266 us (2.4 and
+// 2.1 POPS, 0.71 of twice the bf16 burst and of twice the sustained rate), INT4 with bf16 rows 497 and 571 us (1.11 and
+// 0.96 PFLOP/s, 0.65 and 0.66 of those rates; 449 and 523 us where the rows already lie in order).  32 rows over 8 INT8
+// experts of 4096 x 14336, 466 MB: 72 to 76 us (6.1 TB/s and more, 0.95 of the copy rate).
 #include "grouped.cuh"
 
 #include <algorithm>
@@ -642,10 +642,13 @@ wq_status launch(const CUtensorMap &tx, const CUtensorMap &tw, const Args &a, lo
     return WQ_OK;
 }
 
-// Pair tiles once the experts have rows enough to fill them, measured on B200 by rows per expert.  INT4 (64
-// experts, N = 4096, K = 2048; the other side is grouped_few.cu): 12 rows 150 against 189 us, 20 rows 187
-// against 191, 25 rows 222 against 193.  8 bits (8 experts, N = 4096, K = 14336; the other side are single
-// tiles): 32 rows 80 against 86 us, 48 rows 101 against 87.
+// Pair tiles once the experts have rows enough to fill them, measured on B200 by rows per expert (drawn at random).
+// INT4, the other side being grouped_few.cu with its tiles of 16 rows: 64 experts of 4096 x 2048, bf16, groups of 64,
+// 12 rows 173 against 124 us, 18 rows 173 against 176, 22 rows 173 against 204; 8 experts of 4096 x 14336, fp16, 12 rows
+// 148 against 90, 20 rows 149 against 157, 22 rows 149 against 146.  (The rounding of the weights changes here, so wq.h
+// names the 22.)  8 bits, the other side being single tiles of up to 64 rows: 8 experts of 4096 x 14336, 32 rows 82
+// against 77 us, 48 rows 83 against 79, 64 rows 84 against 96; 64 experts of 4096 x 2048, 32 rows 95 against 91, 48 rows
+// 99 against 94, 64 rows 101 against 112: 36 gives up at most 5% up to about 50 rows.
 template <Kind KIND>
 bool choose_pair(const Args &a) {
     return (long long)a.R >= (is_w4(KIND) ? 22ll : 36ll) * std::min(a.E, a.R);

@@ -15,9 +15,9 @@
 // in contiguous pieces, and the warps' sums meet in shared memory in a fixed order.  A lane holds rows r and r + 8
 // of each block of 16 (r = lane / 4) and a quarter (t = lane % 4) of a chunk's codes.
 //
-// Measured on B200, fp16, groups of 128: 2 of 8 experts of 28672 x 4096 for one token, 122 MB, 37 us (3.3 TB/s; 54 us
-// in grouped_few.cu), 8 experts for 32 rows, 485 MB, 109 us (4.5 TB/s; 152); 64 experts of 4096 x 2048 for 192 rows,
-// 268 MB, 64 us (4.2 TB/s; 90).  No unit is full (issue 0.59 of a slot a cycle and scheduler, integer pipe 53%, tensor
+// Measured on B200, fp16, groups of 128: 2 of 8 experts of 28672 x 4096 for one token, 122 MB, 31 to 33 us (3.8 TB/s; 54
+// us in grouped_few.cu), 8 experts for 32 rows, 485 MB, 104 to 113 us (4.5 TB/s; 152); 64 experts of 4096 x 2048 for 192
+// rows, 268 MB, 65 us (4.1 TB/s; 90).  No unit is full (issue 0.59 of a slot a cycle and scheduler, integer pipe 53%, tensor
 // pipe 28%, HBM 54%), and taking out one part gains little: the conversion 10%, the copies 3%, scales and zero points
 // 7%, x 5%, half of the MMAs nothing.  The last round of tiles costs the rest: 896 tiles for one token are 1.5 rounds.
 #include "grouped.cuh"

@@ -23,9 +23,12 @@ namespace wq {
 namespace {
 
 constexpr int CHUNK = 128;        // tokens ranked at a time: four 32-bit words per expert
-constexpr int ONE_T = 64;         // tokens of a single block (128: 14.7 us; two launches 12.5 us)
-constexpr int CHOOSE_THREADS = 1024;  // 16384 tokens, 128 experts, top 8: 23.0 us, with 512 25.1
-constexpr int THREADS = 512;      // of a block of the second launch (1024: 29 us)
+// Device time in a graph of calls, top 8.  Tokens of a single block: 128 tokens, 64 experts take it 9.9 us, two launches
+// 5.4 us; 64 tokens 5.8 us.
+constexpr int ONE_T = 64;
+// Of a block of the first and of the second launch: 16384 tokens, 128 experts 16.9 us; 512 in the first 17.9 (64 tokens
+// in one block 7.6), 1024 in the second 22.3.
+constexpr int CHOOSE_THREADS = 1024, THREADS = 512;
 constexpr int MIN_PER_BLOCK = 16, MAX_BLOCKS = 256;  // the second launch reads every block's counts
 constexpr int MAX_E = 512, MAX_K = 32, MAX_T = MAX_BLOCKS * 32768;  // counts are 16 bits wide
 constexpr uint32_t KEY_NONE = 0x007FFFFFu;  // key of -inf; keys at or below it are not selectable
