@@ -573,7 +573,8 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, worksp
 
     logits [T, E] fp32, fp16 or bf16 -> (ids int32 [T, k], weights fp32 [T, k], offsets int32 [E + 1],
     rows int32 [T * k], slots int32 [T, k]).  Equal logits go to the lowest expert; NaN and -inf are never chosen
-    (id -1, weight 0, slot -1 where nothing is left).  Expert e's sorted rows are offsets[e]:offsets[e + 1]."""
+    (id -1, weight 0, slot -1 where nothing is left).  Expert e's sorted rows are offsets[e]:offsets[e + 1].  The five
+    results are parts of one allocation, which lives as long as any of them."""
     k = int(top_k)
     _int32(top_k=k)
     _cuda(logits, "logits", (torch.float32, torch.float16, torch.bfloat16), 2)
