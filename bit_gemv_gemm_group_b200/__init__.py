@@ -555,15 +555,14 @@ def _with(first: torch.Tensor, t: torch.Tensor, name: str, dtype, shape) -> None
     raise ValueError(f"{name} is on {t.device}, expected {first.device}")
 
 
-def _int32(**sizes: int) -> None:
+def _int32(what: str, *sizes: int) -> None:
     """Refuses what the C entry points' ints would not hold."""
-    for name, v in sizes.items():
-        if not -(1 << 31) <= v < 1 << 31:
-            raise ValueError(f"{name} ({v}) does not fit 32 bits")
+    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+        raise ValueError(f"{what} {sizes} must fit 32 bits")
 
 
 def moe_route_workspace_bytes(T: int, E: int) -> int:
-    _int32(T=T, E=E)
+    _int32("T, E", T, E)
     return int(lib.wq_moe_route_workspace_bytes(int(T), int(E)))
 
 
@@ -576,13 +575,13 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, worksp
     (id -1, weight 0, slot -1 where nothing is left).  Expert e's sorted rows are offsets[e]:offsets[e + 1].  The five
     results are parts of one allocation, which lives as long as any of them."""
     k = int(top_k)
-    _int32(top_k=k)
+    _int32("top_k", k, k)
     _cuda(logits, "logits", (torch.float32, torch.float16, torch.bfloat16), 2)
     if _elsewhere(logits, stream):
         with _enter(logits, stream):
             return moe_route(logits, top_k, renormalize, workspace)
     T, E = logits.shape
-    _int32(T=T, E=E)
+    _int32("T, E", T, E)
     cols = k if 0 < k <= E else 0              # any other is refused by the call
     need = lib.wq_moe_route_workspace_bytes(T, E)
     n = (T * cols + 3) & ~3                    # one allocation, every part 16-byte aligned; the workspace comes last
@@ -615,7 +614,7 @@ def _grouped(x, offsets, rows, E, N, swiglu, out, dtype):
     if rows is not None:
         R = _cuda(rows, "rows", (torch.int32,), 1).shape[0]
         _with(x, rows, "rows", torch.int32, (R,))
-    _int32(T=T, R=R, N=N, K=x.shape[1])
+    _int32("T, R, N, K", T, R, N, x.shape[1])
     if swiglu and N % 2:
         raise ValueError("the weights must have an even number of rows with swiglu")
     cols = N // 2 if swiglu else N
@@ -715,7 +714,7 @@ def moe_combine(y, weights, slots, out=None, stream=None):
     _cuda(slots, "slots", (torch.int32,), 2)
     T, k = slots.shape
     R, N = y.shape
-    _int32(T=T, top_k=k, R=R, N=N)
+    _int32("T, top_k, R, N", T, k, R, N)
     _with(y, slots, "slots", torch.int32, (T, k))
     _with(y, weights, "weights", torch.float32, (T, k))
     if out is None:
