@@ -575,7 +575,7 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, worksp
     (id -1, weight 0, slot -1 where nothing is left).  Expert e's sorted rows are offsets[e]:offsets[e + 1].  The five
     results are parts of one allocation, which lives as long as any of them."""
     k = int(top_k)
-    _int32("top_k", k, k)
+    _int32("top_k", k)
     _cuda(logits, "logits", (torch.float32, torch.float16, torch.bfloat16), 2)
     if _elsewhere(logits, stream):
         with _enter(logits, stream):
